@@ -66,7 +66,9 @@ typedef enum {
     W4A16_ERR_MISALIGNED = 4,         /* qweight/x/X not 16-byte aligned, ldx % 8 != 0,
                                          scales not 2-byte aligned, y/Y not 4-byte aligned    */
     W4A16_ERR_UNSUPPORTED_DEVICE = 5, /* no current HIP device, or it is not gfx950           */
-    W4A16_ERR_LAUNCH = 6              /* the HIP runtime refused the kernel launch            */
+    W4A16_ERR_LAUNCH = 6,             /* the HIP runtime refused the kernel launch            */
+    W4A16_ERR_BAD_TYPE = 7,           /* a type code names no type the call takes             */
+    W4A16_ERR_WORKSPACE = 8           /* the workspace is smaller than the call needs         */
 } w4a16_status_t;
 
 /*
@@ -253,6 +255,152 @@ w4a16_status_t w4a16_describe_tail_plan(int32_t step, int64_t rows, int64_t K, i
 /* Host-only introspection of w4a16_moe_gemv_batched's launch (same conventions). */
 w4a16_status_t w4a16_describe_moe_batched_plan(int32_t M, int64_t N, int64_t K, int32_t topk,
                                                int32_t cus, char *buf, int64_t len);
+
+/* ---------------------------------------------------------------------------------------------
+ * Token mixers of a decode or prompt step: page tables, the paged key-value cache, attention of
+ * one new token over it, and linear attention. They stand between the weight products above: the
+ * pages name neither, so formats and readings here are this library's own.
+ *
+ * Strides are in elements. Offsets into caches, states and activations are computed in 64 bits.
+ * A workspace is scratch device memory of the caller (16-byte aligned, contents irrelevant before
+ * and after a call); it may be reused by the next call on the same stream.
+ * ------------------------------------------------------------------------------------------- */
+
+typedef enum { W4A16_BF16 = 0, W4A16_FP16 = 1, W4A16_E4M3 = 2 } w4a16_type_t;
+
+/*
+ * A paged key-value cache: `num_pages` pages of `page_size` slots, each slot one row of `dim`
+ * values for each of `heads` KV heads, for keys and for values. Slot s is row s % page_size of page
+ * s / page_size. Rows are contiguous; the other strides are free, so both [page][slot][head][dim]
+ * and [page][head][slot][dim] orders, and K and V interleaved in one buffer, are described by them.
+ *   type: W4A16_BF16, W4A16_FP16, or W4A16_E4M3 (OCP float8 with 3 mantissa bits, NaN 0x7F, largest
+ *   448) with one positive float scale per KV head: value = code * scale (null scales are 1).
+ *   1 <= num_pages, page_size, heads; num_pages * page_size <= 2^31 - 1; heads <= 65535; dim as the
+ *   call says. k, v 16-byte aligned and strides multiples of 16 bytes; scales 4-byte aligned.
+ */
+typedef struct {
+    void *k, *v;
+    int64_t k_stride[3], v_stride[3];   /* page, slot, head */
+    const float *k_scale, *v_scale;     /* float[heads], or null; read for W4A16_E4M3 only */
+    int32_t num_pages, page_size, heads, dim;
+    int32_t type;
+} w4a16_paged_cache_t;
+
+/*
+ * Page tables and slot maps of one step, built on the GPU from the requests' lengths. Request b
+ * holds c_b = max(ctx_lens[b], 0) cached tokens and gets n_b = max(new_lens[b], 0) new ones.
+ * With P(x) = min(ceil(x / page_size), max_pages), it needs pages P(c_b) .. P(c_b + n_b) - 1 of its
+ * row of page_table, which are taken from free_pages in order of the requests:
+ *   page_table[b][j] = free_pages[off_b + j - P(c_b)],  off_b = sum_{a<b} P(c_a + n_a) - P(c_a)
+ *   (-1 where the list is too short); the other entries keep their values.
+ *   seq_lens int32[B] = c_b + n_b;  cu_new int32[B + 1] = 0 and the running sums of n_b;
+ *   for the i-th new token of request b, at t = cu_new[b] + i < max_tokens:
+ *   positions int32[max_tokens]: c_b + i;  slot_map int32[max_tokens]: page * page_size + offset of
+ *   that position, or -1 where the row has no page for it; both are -1 from the last token on.
+ *   counts int32[2]: tokens (sum of n_b) and pages taken (more than num_free: the list was too
+ *   short; more tokens than max_tokens: the last ones have no slot).
+ *   Sums saturate at 2^31 - 1. The call is idempotent while its inputs do not change.
+ *   page_table int32[B] rows of row_stride >= max_pages entries, max_pages >= 1; 1 <= B <= 16384;
+ *   num_free, max_tokens >= 0 (their pointers may be null at 0); 1 <= page_size <= 65536.
+ */
+w4a16_status_t w4a16_page_tables(const int32_t *ctx_lens, const int32_t *new_lens, int32_t B,
+                                 int32_t *page_table, int64_t row_stride, int32_t max_pages,
+                                 const int32_t *free_pages, int32_t num_free, int32_t page_size,
+                                 int32_t max_tokens, int32_t *seq_lens, int32_t *cu_new,
+                                 int32_t *slot_map, int32_t *positions, int32_t *counts,
+                                 hipStream_t stream);
+
+/*
+ * Writes T tokens' keys and values into a paged cache: slot slot_map[t] receives k[t] and v[t]
+ * (a slot outside the cache is skipped). k and v are rows of cache->dim values for each KV head,
+ * token stride ldk / ldv, head stride hsk / hsv, of `type` W4A16_BF16 or W4A16_FP16. The cache has
+ * the same type (bits are copied) or W4A16_E4M3, which receives
+ *   e4m3(min(max(x / scale[head], -448), 448)), the float32 quotient rounded to nearest even.
+ *   NaN stays NaN. Two tokens with one slot leave either row's values there.
+ *   0 <= T; 16 <= dim <= 1024, dim % 16 == 0; k, v 16-byte aligned, strides multiples of 8.
+ */
+w4a16_status_t w4a16_paged_kv_write(const void *k, int64_t ldk, int64_t hsk, const void *v,
+                                    int64_t ldv, int64_t hsv, int32_t T, int32_t type,
+                                    const int32_t *slot_map, const w4a16_paged_cache_t *cache,
+                                    hipStream_t stream);
+
+/*
+ * Attention of one new token of each of B requests over a paged cache. Request b's query head h
+ * reads KV head h / (Hq / cache->heads) at positions lo <= j < n, n = seq_lens[b], lo = 0 or, with
+ * window > 0, max(0, n - window) (the new token is the last position and in the cache already):
+ *   s_j = scale * q[b][h] . k_j;   out[b][h] = sum_j e^{s_j} v_j / sum_j e^{s_j}
+ *   lse[b][h] = log sum_j e^{s_j}  (lse may be null; natural logarithm, contiguous [B][Hq])
+ * A request without positions (n <= 0) has out = +0 and lse = -inf. Positions whose page_table entry
+ * is not a page of the cache, or past max_pages * page_size, contribute nothing. Cache contents
+ * outside the positions read may be anything, NaN included.
+ *   q, out: `type` W4A16_BF16 or W4A16_FP16, Hq heads of dim values, strides ldq/hsq, ldo/hso
+ *   (multiples of 8, 16-byte aligned); cache type the same or W4A16_E4M3.
+ *   page_table int32[B] rows of row_stride >= max_pages >= 1 entries; seq_lens int32[B];
+ *   dim in {64, 96, 128, 192, 256}; Hq % cache->heads == 0, Hq <= 65535; 0 <= B <= 65535;
+ *   max_pages * page_size <= 2^31 - 1; window >= 0; scale finite.
+ *   workspace: w4a16_paged_attention_workspace bytes. Products and sums are held in float32; the
+ *   probabilities enter their product with the values rounded to `type`. Repeated calls give
+ *   identical bits.
+ */
+w4a16_status_t w4a16_paged_attention(const void *q, int64_t ldq, int64_t hsq, int32_t type,
+                                     const w4a16_paged_cache_t *cache, const int32_t *page_table,
+                                     int64_t row_stride, int32_t max_pages,
+                                     const int32_t *seq_lens, int32_t B, int32_t Hq, float scale,
+                                     int32_t window, void *out, int64_t ldo, int64_t hso,
+                                     float *lse, void *workspace, int64_t workspace_bytes,
+                                     hipStream_t stream);
+
+/* Bytes of workspace for w4a16_paged_attention with Hq query heads over `heads` KV heads of `dim`
+ * values, for any batch and length (host only); 0 where the arguments are out of range. */
+int64_t w4a16_paged_attention_workspace(int32_t Hq, int32_t heads, int32_t dim);
+
+/*
+ * Linear attention with a decay for each head, over packed sequences (the form for prompts):
+ *   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale * q_t^T S_t      (S: Dk x Dv, per head)
+ *   q, k: T tokens of Hk heads of Dk values; v, out: T tokens of H heads of Dv values; all of `type`
+ *   W4A16_BF16 or W4A16_FP16, head h reads q and k of head h / (H / Hk); strides multiples of 8,
+ *   16-byte aligned.
+ *   log_decay float: g_t of head h at log_decay[t * ldg + h * hsg]; ldg = 0 gives decays fixed for each
+ *   head. g <= 0 is meant (-inf clears the state); positive values work while e^{sums} stays finite.
+ *   cu_seqlens int32[num_seqs + 1]: sequence s holds tokens cu_seqlens[s] .. cu_seqlens[s+1] - 1 (values
+ *   are clamped to [0, T] and to non-decreasing; tokens outside all sequences are not written).
+ *   cu_seqlens null: one sequence of T tokens, num_seqs == 1.
+ *   state_in float[num_seqs][H][Dk][Dv] or null (zeros); state_out the same layout, fully written
+ *   (a sequence without tokens gets its state_in); state_out == state_in is allowed.
+ *   Dk, Dv in {64, 128}; H % Hk == 0; 0 <= T <= 2^31 - 65; 1 <= num_seqs <= 16384; H <= 32767.
+ *   States, decays and sums are held in float32 or more; within the library the operands of matrix
+ *   products are rounded to `type`, those that reach state_out as a sum of two such values.
+ */
+w4a16_status_t w4a16_linear_attention(const void *q, int64_t ldq, int64_t hsq, const void *k,
+                                      int64_t ldk, int64_t hsk, const void *v, int64_t ldv,
+                                      int64_t hsv, const float *log_decay, int64_t ldg, int64_t hsg,
+                                      const int32_t *cu_seqlens, int32_t num_seqs, int32_t T,
+                                      int32_t Hk, int32_t H, int32_t Dk, int32_t Dv, int32_t type,
+                                      float scale, const float *state_in, float *state_out,
+                                      void *out, int64_t ldo, int64_t hso, void *workspace,
+                                      int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace for w4a16_linear_attention (host only); 0 where none is needed, -1 where the
+ * arguments are out of range. */
+int64_t w4a16_linear_attention_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk,
+                                         int32_t Dv);
+
+/*
+ * The recurrent form of w4a16_linear_attention for one new token of each of B requests: the same
+ * recurrence with t = b. Request b's state is row slots[b] of state_in (row b where slots is null) and
+ * goes to the same row of state_out, which may be state_in. A slot outside [0, num_states) names no
+ * state: out is +0 and no state is touched. Slots of one call have to differ.
+ *   state_in, state_out float[num_states][H][Dk][Dv], 16-byte aligned; num_states >= B where slots is
+ *   null; 0 <= B <= 65535; Dk, Dv, heads, strides and types as above. All arithmetic is float32.
+ */
+w4a16_status_t w4a16_linear_attention_step(const void *q, int64_t ldq, int64_t hsq, const void *k,
+                                           int64_t ldk, int64_t hsk, const void *v, int64_t ldv,
+                                           int64_t hsv, const float *log_decay, int64_t ldg,
+                                           int64_t hsg, const int32_t *slots, int32_t num_states,
+                                           int32_t B, int32_t Hk, int32_t H, int32_t Dk, int32_t Dv,
+                                           int32_t type, float scale, const float *state_in,
+                                           float *state_out, void *out, int64_t ldo, int64_t hso,
+                                           hipStream_t stream);
 
 /* Static, never-NULL description of a status code. */
 const char *w4a16_status_string(w4a16_status_t status);

@@ -12,6 +12,9 @@ Tensor conventions:
   MoE      qweight [E, N, K/8], scales [E, N, K/128], expert_ids torch.int32 [topk] on the GPU,
            out [topk, N]
 
+The token mixers between the weight products (page tables, paged cache, paged attention, linear
+attention) are in mixers.py and reached from here as well.
+
 If libw4a16.so has not been built, every call raises ImportError; there is no fallback.
 """
 from __future__ import annotations
@@ -26,7 +29,10 @@ __all__ = ["gemv", "gemv_batched", "moe_gemv", "moe_gemv_batched", "moe_gemv_swi
            "moe_down_combine", "describe_moe_batched_plan",
            "quantize_pack", "unpack_debug", "describe_plan", "describe_tail_plan", "stream_read",
            "W4A16Error",
-           "library", "LIB_PATH", "GROUP_SIZE", "MAX_BATCH"]
+           "library", "LIB_PATH", "GROUP_SIZE", "MAX_BATCH",
+           "PageTables", "page_tables", "page_tables_buffers", "paged_kv_write", "paged_attention",
+           "paged_attention_workspace", "linear_attention", "linear_attention_workspace",
+           "linear_attention_step"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw4a16.so")
 GROUP_SIZE = 128
@@ -388,3 +394,8 @@ def stream_read(buf: torch.Tensor, nbytes: int, out: torch.Tensor, blocks: int, 
         raise ValueError("out needs blocks * 4 elements")
     _ok(library().w4a16_stream_read(buf.data_ptr(), nbytes, out.data_ptr(), blocks, unroll,
                                     _stream(stream)), "w4a16_stream_read")
+
+
+from .mixers import (PageTables, linear_attention, linear_attention_step,  # noqa: E402
+                     linear_attention_workspace, page_tables, page_tables_buffers, paged_attention,
+                     paged_attention_workspace, paged_kv_write)

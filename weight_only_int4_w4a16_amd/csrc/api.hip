@@ -6,6 +6,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "device.h"
 #include "plan.h"
 #include "w4a16.h"
 
@@ -29,12 +30,6 @@ constexpr int64_t kMaxKDense = 65536;
 constexpr int64_t kMaxKBatched = 1LL << 20;
 constexpr int32_t kMaxTopk = 1024;
 
-struct DeviceInfo {
-    bool ok;
-    int cus;
-    int64_t lds_limit;
-};
-
 std::once_flag g_once[kMaxDevices];
 DeviceInfo g_info[kMaxDevices];
 
@@ -51,7 +46,8 @@ void probe_device(int dev)
     g_info[dev] = info;
 }
 
-// Current device's cached properties, or null when it is missing or not gfx950.
+}  // namespace
+
 const DeviceInfo *current_device()
 {
     int dev = -1;
@@ -60,6 +56,8 @@ const DeviceInfo *current_device()
     std::call_once(g_once[dev], probe_device, dev);
     return g_info[dev].ok ? &g_info[dev] : nullptr;
 }
+
+namespace {
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -389,6 +387,8 @@ const char *w4a16_status_string(w4a16_status_t status)
     case W4A16_ERR_MISALIGNED: return "misaligned pointer or stride";
     case W4A16_ERR_UNSUPPORTED_DEVICE: return "current device is missing or not gfx950";
     case W4A16_ERR_LAUNCH: return "kernel launch failed";
+    case W4A16_ERR_BAD_TYPE: return "type not taken by this call";
+    case W4A16_ERR_WORKSPACE: return "workspace too small";
     }
     return "unknown status";
 }
