@@ -96,68 +96,725 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
         a.Dv == 64 ? step_of<Type, 128, 64>(a, stream) : step_of<Type, 128, 128>(a, stream);
 }
 
-// ---- packed sequences: the recurrence itself -----------------------------------------------------
-// One wave per 64 columns of a head's state and sequence; a lane holds one column.
-template <class Type, int DK>
-__global__ __launch_bounds__(64) void linear_recurrent_kernel(LinearArgs a)
+// ---- packed sequences ----------------------------------------------------------------------------
+// Sequences are cut into segments of L tokens and those into chunks of 64. With b_i the running sum of
+// the log decays inside a chunk (its own token included) and S the state before it, per head:
+//   o_i = scale * (e^{b_i} q_i^T S + sum_{j<=i} e^{b_i - b_j} (q_i . k_j) v_j)
+//   S  <- e^{b_63} S + sum_j k_j (e^{b_63 - b_j} v_j)^T
+// All products are MFMA 16x16x32. A wave owns 32 of the Dv columns, with its part of S in registers in
+// float32, so waves share nothing but the chunk's q and k in LDS; every wave forms all the scores.
+//
+// Operands never cross lanes. A contraction's order is free as long as both operands agree:
+//   scores are formed transposed (k q^T): a lane then holds token i = lane % 16 of a tile of queries and
+//   the keys 4g..4g+3 (g = lane / 16) of a tile of 16; two such tiles are the first operand of the
+//   product with v for the keys {4g..4g+3, 16 + 4g..16 + 4g+3} of 32, and v rows are taken in that order;
+//   the state's tile j has rows dk = EK m + j (EK = Dk / 16, m = 4g + r in a lane), as a lane's EK
+//   consecutive values of k rows give them; two tiles are the second operand of the product q S, whose
+//   first operand, q at dk = EK (4g + r) + {j, j + 1}, are words that the lane has loaded for the scores.
+//
+// Roundings: scores with their decay, S in q S, and e^{b_63 - b_j} v_j are rounded to the type for
+// their products, the last one kept as a sum of two values where the result reaches a returned
+// state. Decays are summed in float64 per chunk and kept as two floats, so far jumps (a state cleared
+// by -inf, which counts as -10^4 per token) do not cost the others their digits.
+//
+// One segment per sequence needs one launch. Longer ones take three: what each segment but the last
+// adds to a state (K and V read once), the states before every segment (a running sum over
+// segments), then the outputs of all segments side by side.
+constexpr int kChunk = 64;
+constexpr int kWaveSeqs = 64;   // up to here every wave finds its segment by itself
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f32x4 mfma(Bf16, u32x4 a, u32x4 b, f32x4 c)
 {
-    typedef typename Type::T T;
-    __shared__ float qs[DK], ks[DK];
-    const int lane = threadIdx.x, parts = a.Dv / 64;
-    const int h = blockIdx.x / parts, c = (blockIdx.x % parts) * 64 + lane;
-    const int64_t b = blockIdx.y;
-    int32_t t0 = 0, t1 = a.T;
-    if (a.cu) {
-        for (int s = 0; s <= b; ++s)
-            t0 = max(t0, min(a.cu[s], a.T));
-        t1 = max(t0, min(a.cu[b + 1], a.T));
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma(Fp16, u32x4 a, u32x4 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t pack2(Bf16, float a, float b)
+{
+    const bf16x2 r = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ uint32_t pack2(Fp16, float a, float b)
+{
+    const f16x2 r = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ float low(Bf16, uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float high(Bf16, uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+__device__ __forceinline__ float low(Fp16, uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[0]; }
+__device__ __forceinline__ float high(Fp16, uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[1]; }
+
+// What is left of (a, b) after rounding to the packed pair `w`. A float16 remainder is kept 2^11 times
+// as large, so that it does not fall among the subnormals, and meets k times 2^-11.
+__device__ __forceinline__ uint32_t rest2(Bf16 t, float a, float b, uint32_t w)
+{
+    return pack2(t, a - low(t, w), b - high(t, w));
+}
+__device__ __forceinline__ uint32_t rest2(Fp16 t, float a, float b, uint32_t w)
+{
+    return pack2(t, (a - low(t, w)) * 2048.0f, (b - high(t, w)) * 2048.0f);
+}
+__device__ __forceinline__ u32x4 for_rest(Bf16, u32x4 k) { return k; }
+__device__ __forceinline__ u32x4 for_rest(Fp16, u32x4 k)
+{
+    return __builtin_bit_cast(u32x4, __builtin_bit_cast(f16x8, k) * (_Float16)(1.0f / 2048.0f));
+}
+
+// Whether either value of the pairs seen is not finite: the exponent field, plus one unit of it,
+// carries into the sign's place. And a pair with zeros in the place of such values.
+__device__ __forceinline__ uint32_t odd_bits(Bf16, uint32_t w) { return (w & 0x7FFF7FFFu) + 0x00800080u; }
+__device__ __forceinline__ uint32_t odd_bits(Fp16, uint32_t w) { return (w & 0x7FFF7FFFu) + 0x04000400u; }
+template <class Type>
+__device__ __forceinline__ uint32_t only_finite(Type t, uint32_t w)
+{
+    const uint32_t o = odd_bits(t, w);
+    return w & ((o & 0x8000u ? 0u : 0xFFFFu) | (o & 0x80000000u ? 0u : 0xFFFF0000u));
+}
+
+// The power of two that brings values up to `most` below 2^15 in float16 (bfloat16 needs none).
+__device__ __forceinline__ float fit(Bf16, float) { return 1.0f; }
+__device__ __forceinline__ float fit(Fp16, float most)
+{
+    if (!(most < INFINITY) || most < 0x1p-100f)
+        return 1.0f;
+    return __builtin_ldexpf(1.0f, 15 - __builtin_amdgcn_frexp_expf(most));
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double x)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)u, CTRL, ROWS, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xF, true);
+    return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Running sum over the 64 lanes: shifts by 1, 2, 4, 8 inside rows of 16, then the rows' ends.
+__device__ __forceinline__ double running_sum(double x)
+{
+    x = dpp_add<0x111, 0xF>(x);
+    x = dpp_add<0x112, 0xF>(x);
+    x = dpp_add<0x114, 0xF>(x);
+    x = dpp_add<0x118, 0xF>(x);
+    x = dpp_add<0x142, 0xA>(x);
+    return dpp_add<0x143, 0xC>(x);
+}
+
+struct Cuts {           // how a call's sequences are cut
+    int32_t L;          // tokens per segment, a multiple of kChunk
+    int32_t starts;     // segments that are not their sequence's last, at most
+    int32_t slots;      // states in the workspace: one per segment of a sequence that has several, at most
+    int32_t *maps;      // more than kWaveSeqs sequences: [3][num_seqs + 1] starts, segments, slots before each
+    float *states;      // [slots][H][Dk][Dv]
+    float *decays;      // [slots][H]: a segment's whole decay
+};
+
+struct Segment {
+    int32_t seq, index, last;   // sequence, number inside it, whether it is the sequence's last one
+    int32_t t0, t1;             // tokens
+    int32_t slot;               // state slot of the segment, where the sequence has several
+};
+
+// Segment number `unit` of all (inner: of those that are not their sequence's last). A sequence
+// without tokens has one segment. False past the end.
+__device__ bool find_segment(const LinearArgs &a, const Cuts &c, int unit, bool inner, Segment *s)
+{
+    int32_t start, end, slot0;
+    if (!a.cu) {
+        s->seq = 0;
+        start = 0;
+        end = a.T;
+        s->index = unit;
+        slot0 = 0;
+        const int32_t n = max(1, (int32_t)(((int64_t)a.T + c.L - 1) / c.L));
+        if (unit >= n - (inner ? 1 : 0))
+            return false;
+    } else if (a.B <= kWaveSeqs) {
+        const int lane = threadIdx.x & 63;
+        const int at = min(lane, a.B);
+        int32_t x = min(max(a.cu[at], 0), a.T), y = min(max(a.cu[min(at + 1, a.B)], 0), a.T);
+        for (int d = 1; d < 64; d <<= 1) {   // running maximum of the starts
+            const int32_t o = __shfl_up(x, d);
+            if (lane >= d)
+                x = max(x, o);
+        }
+        y = max(x, y);
+        const int32_t n = lane < a.B ? max(1, (int32_t)(((int64_t)(y - x) + c.L - 1) / c.L)) : 0;
+        int32_t before = n;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int32_t o = __shfl_up(before, d);
+            if (lane >= d)
+                before += o;
+        }
+        before -= n;
+        const uint64_t single = __ballot(n == 1);   // these need no slots
+        const int32_t slots = before - __builtin_popcountll(single & ((1ull << lane) - 1));
+        const int32_t key = inner ? before - min(lane, a.B) : before;
+        const uint64_t hit = __ballot(lane < a.B && key <= unit);
+        const int seq = 63 - __builtin_clzll(hit);   // lane 0's key is 0
+        s->seq = seq;
+        start = __builtin_amdgcn_readlane(x, seq);
+        end = __builtin_amdgcn_readlane(y, seq);
+        s->index = unit - __builtin_amdgcn_readlane(key, seq);
+        slot0 = __builtin_amdgcn_readlane(slots, seq);
+        if (s->index >= __builtin_amdgcn_readlane(n, seq) - (inner ? 1 : 0))
+            return false;
+    } else {
+        const int32_t *starts = c.maps, *segments = starts + a.B + 1, *slots = segments + a.B + 1;
+        if (unit >= segments[a.B] - (inner ? a.B : 0))
+            return false;
+        int lo = 0, hi = a.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (segments[mid] - (inner ? mid : 0) <= unit)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        s->seq = lo;
+        start = starts[lo];
+        end = max(start, min(max(a.cu[lo + 1], 0), a.T));
+        s->index = unit - (segments[lo] - (inner ? lo : 0));
+        slot0 = slots[lo];
     }
-    const int64_t base = (b * a.H + h) * (int64_t)DK * a.Dv + c;
-    float s[DK];
-#pragma unroll
-    for (int r = 0; r < DK; ++r)
-        s[r] = a.state_in ? a.state_in[base + (int64_t)r * a.Dv] : 0.0f;
+    s->slot = slot0 + s->index;
+    s->t0 = (int32_t)min((int64_t)start + (int64_t)s->index * c.L, (int64_t)end);
+    s->last = end - s->t0 <= c.L;
+    s->t1 = s->last ? end : s->t0 + c.L;
+    return true;
+}
+
+// The running sums that find_segment searches, for many sequences: one work-group.
+constexpr int kMapThreads = 1024;
+__global__ __launch_bounds__(kMapThreads) void linear_maps_kernel(LinearArgs a, Cuts c)
+{
+    __shared__ int32_t wave_x[kMapThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int32_t *starts = c.maps, *segments = starts + a.B + 1, *slots = segments + a.B + 1;
+    __shared__ int32_t wave_one[kMapThreads / 64];
+    int32_t top = 0, sum = 0, ones = 0;   // before this round of kMapThreads sequences
+    for (int b0 = 0; b0 < a.B; b0 += kMapThreads) {
+        const int b = b0 + tid;
+        int32_t x = b < a.B ? min(max(a.cu[b], 0), a.T) : 0;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int32_t o = __shfl_up(x, d);
+            if (lane >= d)
+                x = max(x, o);
+        }
+        __syncthreads();
+        if (lane == 63)
+            wave_x[wave] = x;
+        __syncthreads();
+        x = max(x, top);
+        for (int w = 0; w < kMapThreads / 64; ++w) {
+            if (w < wave)
+                x = max(x, wave_x[w]);
+            top = max(top, wave_x[w]);
+        }
+        int32_t n = 0;
+        if (b < a.B) {
+            const int32_t y = max(x, min(max(a.cu[b + 1], 0), a.T));
+            n = max(1, (int32_t)(((int64_t)(y - x) + c.L - 1) / c.L));
+        }
+        int32_t s = n;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int32_t o = __shfl_up(s, d);
+            if (lane >= d)
+                s += o;
+        }
+        const uint64_t single = __ballot(n == 1);
+        int32_t one = ones + __builtin_popcountll(single & ((1ull << lane) - 1));
+        __syncthreads();
+        if (lane == 63) {
+            wave_x[wave] = s;
+            wave_one[wave] = __builtin_popcountll(single);
+        }
+        __syncthreads();
+        s += sum - n;
+        for (int w = 0; w < kMapThreads / 64; ++w) {
+            if (w < wave) {
+                s += wave_x[w];
+                one += wave_one[w];
+            }
+            sum += wave_x[w];
+            ones += wave_one[w];
+        }
+        if (b < a.B) {
+            starts[b] = x;
+            segments[b] = s;
+            slots[b] = s - one;   // single segments need none
+        }
+    }
+    if (tid == 0) {
+        segments[a.B] = sum;
+        slots[a.B] = sum - ones;
+    }
+}
+
+// One segment of one head. OUT: its outputs, and the final state where it is the sequence's last;
+// otherwise (segments with a slot) what it adds to the state, and its whole decay.
+template <class Type, int DK, int DV, bool OUT>
+__global__ __launch_bounds__(64 * (DV / 32), 2) void linear_chunk_kernel(LinearArgs a, Cuts cuts)
+{
+    constexpr int NW = DV / 32, threads = 64 * NW, EK = DK / 16, WK = EK / 2;
+    constexpr int pieces = DK / 8, loads = kChunk * pieces / threads, stride = DK + 8;
+    constexpr int contractions = DK / 32;
+    __shared__ __align__(16) uint16_t qs[OUT ? kChunk : 1][stride];
+    __shared__ __align__(16) uint16_t ks[kChunk][stride];
+    // per token: b (two floats, log2), scale e^b, e^(b_63 - b)
+    __shared__ __align__(16) float bh[kChunk], bl[kChunk], eb[kChunk], ed[kChunk];
+    __shared__ uint32_t odd_k[NW];   // a wave's part of k holds values that are not finite
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 15, g = lane >> 4, h = blockIdx.x;
+    Segment seg;
+    if (!find_segment(a, cuts, blockIdx.y, !OUT, &seg))
+        return;
     const int hk = h / (a.H / a.Hk);
-    for (int64_t t = t0; t < t1; ++t) {
-        __syncthreads();
-        for (int r = lane; r < DK; r += 64) {
-            qs[r] = a.scale * Type::f(((const T *)a.q)[t * a.ldq + hk * a.hsq + r]);
-            ks[r] = Type::f(((const T *)a.k)[t * a.ldk + hk * a.hsk + r]);
-        }
-        __syncthreads();
-        const float v = Type::f(((const T *)a.v)[t * a.ldv + h * a.hsv + c]);
-        const float decay = expf(a.g[t * a.ldg + h * a.hsg]);
-        float acc = 0.0f;
+    const uint16_t *qp = (const uint16_t *)a.q + hk * a.hsq, *kp = (const uint16_t *)a.k + hk * a.hsk;
+    const uint16_t *vp = (const uint16_t *)a.v + h * a.hsv + wave * 32 + 2 * col;
+    const float *gp = a.g + h * a.hsg;
+    const int64_t state_at = (int64_t)(4 * g * EK) * DV + wave * 32 + 2 * col;   // of s[0][.][0]
+    const int64_t state_size = (int64_t)DK * DV;
+
+    // s[j][t][r]: row EK (4g + r) + j, column 32 wave + 2 col + t
+    f32x4 s[EK][2];
+    const float *from = nullptr;
+    if (OUT && (seg.index > 0 || !seg.last))
+        from = cuts.states + ((int64_t)seg.slot * a.H + h) * state_size + state_at;
+    else if (OUT && a.state_in)
+        from = a.state_in + ((int64_t)seg.seq * a.H + h) * state_size + state_at;
 #pragma unroll
-        for (int r = 0; r < DK; ++r) {
-            s[r] = fmaf(ks[r], v, decay * s[r]);
-            acc = fmaf(qs[r], s[r], acc);
+    for (int j = 0; j < EK; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            f32x2 x = {0.0f, 0.0f};
+            if (from)
+                x = *(const f32x2 *)(from + (int64_t)(EK * r + j) * DV);
+            s[j][0][r] = x[0];
+            s[j][1][r] = x[1];
         }
-        ((T *)a.out)[t * a.ldo + h * a.hso + c] = Type::from(acc);
+
+    u32x4 qn[OUT ? loads : 1], kn[loads];
+    uint32_t vn[16];
+    float gn = 0.0f;
+    auto fetch = [&](int32_t t) {   // a chunk's rows; zeros past the segment's end
+        const int32_t n = seg.t1 - t;
+#pragma unroll
+        for (int i = 0; i < loads; ++i) {
+            const int piece = tid + i * threads, row = piece / pieces, d = (piece % pieces) * 8;
+            const int64_t tok = t + min(row, n - 1);
+            if (OUT)
+                qn[i] = *(const u32x4 *)(qp + tok * a.ldq + d);
+            kn[i] = *(const u32x4 *)(kp + tok * a.ldk + d);
+            if (row >= n) {
+                kn[i] = u32x4{0, 0, 0, 0};
+                if (OUT)
+                    qn[i] = u32x4{0, 0, 0, 0};
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int row = 32 * (e / 8) + 16 * ((e / 4) & 1) + 4 * g + (e & 3);
+            const int64_t tok = t + min(row, n - 1);
+            vn[e] = *(const uint32_t *)(vp + tok * a.ldv);
+            if (row >= n)
+                vn[e] = 0;
+        }
+        const int64_t tok = t + min(lane, n - 1);
+        gn = gp[tok * a.ldg];
+        if (lane >= n)
+            gn = 0.0f;
+    };
+
+    double whole = 0.0;   // sum of log2 decays of the segment
+    if (seg.t0 < seg.t1)
+        fetch(seg.t0);
+    for (int32_t t = seg.t0; t < seg.t1; t += kChunk) {
+        const int32_t n = seg.t1 - t;
+        const float gc = gn < -1.0e4f ? -1.0e4f : gn;
+        const double b = running_sum((double)gc * 1.44269504088896340736);
+        const uint64_t bu = __builtin_bit_cast(uint64_t, b);
+        const double end = __builtin_bit_cast(
+            double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(bu >> 32), 63) << 32 |
+                        (uint32_t)__builtin_amdgcn_readlane((int)bu, 63));
+        const float whole_chunk = __builtin_amdgcn_exp2f((float)end);
+        whole += end;
+        __syncthreads();   // the previous chunk has been read
+        uint32_t odd = 0;
+#pragma unroll
+        for (int i = 0; i < loads; ++i) {
+            const int piece = tid + i * threads, row = piece / pieces, d = (piece % pieces) * 8;
+            if (OUT)
+                *(u32x4 *)&qs[row][d] = qn[i];
+            *(u32x4 *)&ks[row][d] = kn[i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                odd |= odd_bits(Type(), kn[i][e]);
+        }
+        odd = __ballot((odd & 0x80008000u) != 0) != 0;
+        if (lane == 0)
+            odd_k[wave] = odd;
+        odd = 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            odd |= odd_bits(Type(), vn[e]);
+        const bool odd_v = __ballot((odd & 0x80008000u) != 0) != 0;
+        if (wave == 0) {
+            if (OUT) {
+                const float hi = (float)b;
+                bh[lane] = hi;
+                bl[lane] = (float)(b - hi);
+                eb[lane] = a.scale * __builtin_amdgcn_exp2f(hi);
+            }
+            ed[lane] = __builtin_amdgcn_exp2f((float)(end - b));
+        }
+        u32x4 v[2][2];   // [half of the chunk][column parity]: second operands
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t x0 = vn[8 * half + 2 * e], x1 = vn[8 * half + 2 * e + 1];
+                v[half][0][e] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
+                v[half][1][e] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
+            }
+        __syncthreads();
+        if (n > kChunk)
+            fetch(t + kChunk);
+        bool odd_any = odd_v;
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            odd_any |= odd_k[w] != 0;
+        odd_any = __builtin_amdgcn_readfirstlane(odd_any);
+        __builtin_amdgcn_sched_barrier(0);
+
+        if (OUT) {
+            float most = 0.0f;
+            if constexpr (sizeof(Type) && __is_same(Type, Fp16)) {
+#pragma unroll
+                for (int j = 0; j < EK; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        most = fmaxf(most, fmaxf(fabsf(s[j][0][r]), fabsf(s[j][1][r])));
+                for (int d = 1; d < 64; d <<= 1)
+                    most = fmaxf(most, __shfl_xor(most, d));
+            }
+            const float shrink = fit(Type(), most), grow = 1.0f / shrink;
+            u32x4 sp[WK][2];   // the state as second operands
+#pragma unroll
+            for (int p = 0; p < WK; ++p)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        sp[p][c][r] = pack2(Type(), s[2 * p][c][r] * shrink, s[2 * p + 1][c][r] * shrink);
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                if (it * 16 >= n)
+                    break;
+                u32x4 q[contractions];   // dims (Dk / 4) g .. + Dk / 4 of token 16 it + col
+#pragma unroll
+                for (int c = 0; c < contractions; ++c)
+                    q[c] = *(const u32x4 *)&qs[16 * it + col][DK / 4 * g + 8 * c];
+                f32x4 o[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+                for (int p = 0; p < WK; ++p) {
+                    u32x4 x;   // words of dims EK r + 2p of the lane's
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        x[r] = q[(WK * r + p) / 4][(WK * r + p) % 4];
+                    o[0] = mfma(Type(), x, sp[p][0], o[0]);
+                    o[1] = mfma(Type(), x, sp[p][1], o[1]);
+                }
+                const f32x4 row = *(const f32x4 *)&eb[16 * it + 4 * g];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    o[0][r] *= row[r] * grow;
+                    o[1][r] *= row[r] * grow;
+                }
+                const float bhi = bh[16 * it + col], blo = bl[16 * it + col];
+#pragma unroll
+                for (int half = 0; half <= it / 2; ++half) {
+                    u32x4 w = {0, 0, 0, 0};   // scores of token 16 it + col with 8 keys of the half
+#pragma unroll
+                    for (int k = 0; k < 2 && 2 * half + k <= it; ++k) {
+                        const int jt = 2 * half + k;
+                        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int c = 0; c < contractions; ++c)
+                            x = mfma(Type(), *(const u32x4 *)&ks[16 * jt + col][DK / 4 * g + 8 * c], q[c], x);
+                        const f32x4 jh = *(const f32x4 *)&bh[16 * jt + 4 * g];
+                        const f32x4 jl = *(const f32x4 *)&bl[16 * jt + 4 * g];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float d = __builtin_amdgcn_exp2f((bhi - jh[r]) + (blo - jl[r]));
+                            x[r] = jt < it || 4 * g + r <= col ? x[r] * (a.scale * d) : 0.0f;
+                        }
+                        w[2 * k] = pack2(Type(), x[0], x[1]);
+                        w[2 * k + 1] = pack2(Type(), x[2], x[3]);
+                    }
+                    if (odd_v && half == it / 2) {
+                        // A later token's infinity must not meet an earlier one's zero weight: each
+                        // token of the tile by itself, with the rows after it cleared.
+                        for (int m = 0; m < 16; ++m)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                u32x4 x = v[half][c];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int key = 32 * half + 16 * (e / 2) + 4 * g + 2 * (e & 1), i = 16 * it + m;
+                                    x[e] = key > i ? 0u : key + 1 > i ? x[e] & 0xFFFFu : x[e];
+                                }
+                                const f32x4 y = mfma(Type(), w, x, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    if (4 * g + r == m)
+                                        o[c][r] += y[r];
+                            }
+                    } else {
+                        o[0] = mfma(Type(), w, v[half][0], o[0]);
+                        o[1] = mfma(Type(), w, v[half][1], o[1]);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 16 * it + 4 * g + r;
+                    if (i < n)
+                        *(uint32_t *)((uint16_t *)a.out + (int64_t)(t + i) * a.ldo + h * a.hso + wave * 32 + 2 * col) =
+                            pack2(Type(), o[0][r], o[1][r]);
+                }
+            }
+        }
+
+        if (OUT && n <= kChunk && !seg.last)
+            break;   // nobody reads the state after this segment
+#pragma unroll
+        for (int j = 0; j < EK; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                s[j][0][r] *= whole_chunk;
+                s[j][1][r] *= whole_chunk;
+            }
+        const bool rest = !OUT || seg.last;   // the state is returned, or starts others
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            u32x4 x[2], y[2];   // e^(b_63 - b_j) v_j and what its rounding leaves
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f32x2 d = *(const f32x2 *)&ed[32 * half + 16 * (e / 2) + 4 * g + 2 * (e & 1)];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float v0 = low(Type(), v[half][c][e]) * d[0], v1 = high(Type(), v[half][c][e]) * d[1];
+                    uint32_t both = pack2(Type(), v0, v1);
+                    // The remainder goes by the bits that the product gets: left to itself, the compiler
+                    // rounds v * d once for one use and twice (float32 first) for the other.
+                    asm volatile("" : "+v"(both));
+                    x[c][e] = both;
+                    y[c][e] = rest2(Type(), v0, v1, x[c][e]);
+                }
+            }
+            uint32_t rows[8][WK];   // dims EK col .. of the half's eight keys
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint16_t *p = &ks[32 * half + 16 * (e / 4) + 4 * g + (e & 3)][EK * col];
+                if constexpr (WK == 4) {
+                    const u32x4 x = *(const u32x4 *)p;
+                    rows[e][0] = x[0]; rows[e][1] = x[1]; rows[e][2] = x[2]; rows[e][3] = x[3];
+                } else {
+                    const u32x2 x = *(const u32x2 *)p;
+                    rows[e][0] = x[0]; rows[e][1] = x[1];
+                }
+            }
+            if (odd_any && rest) {   // an infinity's rounding leaves nothing
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t o = odd_bits(Type(), x[c][e]);
+                        y[c][e] &= (o & 0x8000u ? 0u : 0xFFFFu) | (o & 0x80000000u ? 0u : 0xFFFF0000u);
+                    }
+            }
+#pragma unroll
+            for (int w = 0; w < WK; ++w) {
+                u32x4 k0, k1;   // dims EK col + 2w and + 2w + 1
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    k0[e] = __builtin_amdgcn_perm(rows[2 * e + 1][w], rows[2 * e][w], 0x05040100u);
+                    k1[e] = __builtin_amdgcn_perm(rows[2 * e + 1][w], rows[2 * e][w], 0x07060302u);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    s[2 * w][c] = mfma(Type(), k0, x[c], s[2 * w][c]);
+                    s[2 * w + 1][c] = mfma(Type(), k1, x[c], s[2 * w + 1][c]);
+                }
+                if (rest) {
+                    if (odd_any) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            k0[e] = only_finite(Type(), k0[e]);
+                            k1[e] = only_finite(Type(), k1[e]);
+                        }
+                    }
+                    k0 = for_rest(Type(), k0);
+                    k1 = for_rest(Type(), k1);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        s[2 * w][c] = mfma(Type(), k0, y[c], s[2 * w][c]);
+                        s[2 * w + 1][c] = mfma(Type(), k1, y[c], s[2 * w + 1][c]);
+                    }
+                }
+            }
+        }
     }
+
+    if (OUT && !seg.last)
+        return;
+    float *to = OUT ? a.state_out + ((int64_t)seg.seq * a.H + h) * state_size
+                    : cuts.states + ((int64_t)(seg.slot + 1) * a.H + h) * state_size;
 #pragma unroll
-    for (int r = 0; r < DK; ++r)
-        a.state_out[base + (int64_t)r * a.Dv] = s[r];
+    for (int j = 0; j < EK; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            *(f32x2 *)(to + state_at + (int64_t)(EK * r + j) * DV) = f32x2{s[j][0][r], s[j][1][r]};
+    if (!OUT && tid == 0)
+        cuts.decays[(int64_t)(seg.slot + 1) * a.H + h] = __builtin_amdgcn_exp2f((float)whole);
+}
+
+// The state before every segment of a sequence that has several: its slot holds what the segment
+// before it adds, and then that state (the first one's: state_in, which the sequence's last segment
+// may overwrite). Four elements per thread, the additions of four segments in flight.
+__global__ __launch_bounds__(256) void linear_states_kernel(LinearArgs a, Cuts c)
+{
+    const int32_t size = a.Dk * a.Dv;
+    const int h = blockIdx.x, part = blockIdx.z;
+    int32_t slot0, n;
+    const int seq = blockIdx.y;
+    if (!a.cu) {
+        slot0 = 0;
+        n = (int32_t)(((int64_t)a.T + c.L - 1) / c.L);
+    } else if (a.B <= kWaveSeqs) {
+        int32_t top = 0, total = 0;   // few sequences: a walk over their starts
+        slot0 = n = 0;
+        for (int s = 0; s <= seq; ++s) {
+            top = max(top, min(max(a.cu[s], 0), a.T));
+            const int32_t y = max(top, min(max(a.cu[s + 1], 0), a.T));
+            n = (int32_t)(((int64_t)(y - top) + c.L - 1) / c.L);
+            slot0 = total;
+            total += n > 1 ? n : 0;
+        }
+    } else {
+        const int32_t *slots = c.maps + 2 * (a.B + 1);
+        slot0 = slots[seq];
+        n = slots[seq + 1] - slot0;
+    }
+    if (n <= 1)
+        return;
+    const int32_t at = (part * 256 + (int)threadIdx.x) * 4;
+    const int64_t step = (int64_t)a.H * size;
+    float *p = c.states + ((int64_t)slot0 * a.H + h) * size + at;
+    const float *d = c.decays + (int64_t)slot0 * a.H + h;
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.state_in)
+        s = *(const f32x4 *)(a.state_in + ((int64_t)seq * a.H + h) * size + at);
+    *(f32x4 *)p = s;
+    constexpr int U = 4;
+    for (int k = 1; k < n; k += U) {
+        f32x4 x[U];
+        float f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k + u < n) {
+                x[u] = *(const f32x4 *)(p + (k + u) * step);
+                f[u] = d[(int64_t)(k + u) * a.H];
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k + u < n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[e] = fmaf(f[u], s[e], x[u][e]);
+                *(f32x4 *)(p + (k + u) * step) = s;
+            }
+    }
+}
+
+template <class Type, int DK, int DV>
+hipError_t linear_of(const LinearArgs &a, const Cuts &c, hipStream_t stream)
+{
+    const dim3 block(64 * (DV / 32));
+    if (a.cu && a.B > kWaveSeqs)
+        linear_maps_kernel<<<dim3(1), dim3(kMapThreads), 0, stream>>>(a, c);
+    if (c.starts > 0) {
+        linear_chunk_kernel<Type, DK, DV, false><<<dim3(a.H, c.starts), block, 0, stream>>>(a, c);
+        linear_states_kernel<<<dim3(a.H, a.B, DK * DV / 1024), dim3(256), 0, stream>>>(a, c);
+    }
+    linear_chunk_kernel<Type, DK, DV, true><<<dim3(a.H, c.starts + a.B), block, 0, stream>>>(a, c);
+    return hipGetLastError();
 }
 
 template <class Type>
-void linear_typed(const LinearArgs &a, hipStream_t stream)
+hipError_t linear_typed(const LinearArgs &a, const Cuts &c, hipStream_t stream)
 {
-    const dim3 grid(a.H * (a.Dv / 64), a.B), block(64);
     if (a.Dk == 64)
-        linear_recurrent_kernel<Type, 64><<<grid, block, 0, stream>>>(a);
-    else
-        linear_recurrent_kernel<Type, 128><<<grid, block, 0, stream>>>(a);
+        return a.Dv == 64 ? linear_of<Type, 64, 64>(a, c, stream) : linear_of<Type, 64, 128>(a, c, stream);
+    return a.Dv == 64 ? linear_of<Type, 128, 64>(a, c, stream) : linear_of<Type, 128, 128>(a, c, stream);
+}
+
+// Tokens per segment: enough segments for two work-groups per CU of a 256-CU device, but not so short
+// that reading and writing their states (256 KB per segment and head of 128 x 128, against 1.5 KB per
+// token) weighs, and no more segments than the grid takes.
+int32_t segment_length(int32_t T, int32_t H)
+{
+    int64_t L = ((int64_t)T * H / 512 + kChunk - 1) / kChunk * kChunk;
+    if (L < 512)
+        L = 512;
+    if (L > 4096)
+        L = 4096;
+    while (T / L > 32768)
+        L *= 2;
+    return (int32_t)L;
+}
+
+int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
+
+// A sequence of several segments has x + 1 <= 2x of them, x the whole segments before its last token,
+// and all such x sum up to at most T / L.
+Cuts cuts_of(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk, int32_t Dv, float *work, int64_t *bytes)
+{
+    Cuts c;
+    c.L = segment_length(T, H);
+    c.starts = T / c.L;
+    c.slots = 2 * c.starts;
+    const int64_t states = (int64_t)c.slots * H * Dk * Dv * 4, decays = round16((int64_t)c.slots * H * 4);
+    const int64_t maps = num_seqs > kWaveSeqs ? round16(3 * ((int64_t)num_seqs + 1) * 4) : 0;
+    c.states = work;
+    c.decays = (float *)((char *)work + states);
+    c.maps = (int32_t *)((char *)c.decays + decays);
+    *bytes = states + decays + maps;
+    return c;
 }
 
 }  // namespace
 
-int64_t linear_workspace(int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+int64_t linear_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk, int32_t Dv)
+{
+    int64_t bytes;
+    cuts_of(T, num_seqs, H, Dk, Dv, nullptr, &bytes);
+    return bytes;
+}
 
 hipError_t launch_linear(const LinearArgs &a, int, hipStream_t stream)
 {
-    a.type ? linear_typed<Fp16>(a, stream) : linear_typed<Bf16>(a, stream);
-    return hipGetLastError();
+    int64_t bytes;
+    const Cuts c = cuts_of(a.T, a.B, a.H, a.Dk, a.Dv, a.work, &bytes);
+    return a.type ? linear_typed<Fp16>(a, c, stream) : linear_typed<Bf16>(a, c, stream);
 }
 
 hipError_t launch_linear_step(const LinearArgs &a, int, hipStream_t stream)
