@@ -359,7 +359,7 @@ int64_t w4a16_paged_attention_workspace(int32_t Hq, int32_t heads, int32_t dim);
  *   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale * q_t^T S_t      (S: Dk x Dv, per head)
  *   q, k: T tokens of Hk heads of Dk values; v, out: T tokens of H heads of Dv values; all of `type`
  *   W4A16_BF16 or W4A16_FP16, head h reads q and k of head h / (H / Hk); strides multiples of 8,
- *   16-byte aligned.
+ *   16-byte aligned; token strides (and ldg) from 0 to 2^24 - 1.
  *   log_decay float: g_t of head h at log_decay[t * ldg + h * hsg]; ldg = 0 gives decays fixed for each
  *   head. g <= 0 is meant (-inf clears the state); positive values work while e^{sums} stays finite.
  *   cu_seqlens int32[num_seqs + 1]: sequence s holds tokens cu_seqlens[s] .. cu_seqlens[s+1] - 1 (values

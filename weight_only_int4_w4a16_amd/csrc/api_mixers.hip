@@ -53,6 +53,9 @@ w4a16_status_t check_linear(const LinearArgs &a)
         return W4A16_ERR_BAD_TYPE;
     if (!known_linear(a.Hk, a.H, a.Dk, a.Dv) || !isfinite(a.scale))
         return W4A16_ERR_BAD_SHAPE;
+    for (int64_t ld : {a.ldq, a.ldk, a.ldv, a.ldg, a.ldo})   // a chunk's rows lie within 32-bit offsets
+        if (ld < 0 || ld >= 1 << 24)
+            return W4A16_ERR_BAD_SHAPE;
     if (!aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.out, 16) ||
         !aligned(a.g, 4) || !aligned(a.cu, 4) || !aligned(a.state_in, 16) || !aligned(a.state_out, 16) ||
         !strided8(a.ldq, a.hsq) || !strided8(a.ldk, a.hsk) || !strided8(a.ldv, a.hsv) ||

@@ -114,13 +114,15 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 //
 // Roundings: scores with their decay, S in q S, and e^{b_63 - b_j} v_j are rounded to the type for
 // their products, the last one kept as a sum of two values where the result reaches a returned
-// state. Decays are summed in float64 per chunk and kept as two floats, so far jumps (a state cleared
-// by -inf, which counts as -10^4 per token) do not cost the others their digits.
+// state. Decays are summed in float64 over a chunk; the scores' take the sums in float32, off by 2^-24
+// of their size. A log decay below -104 counts as that: e^-104 is zero in float32, and so a state that
+// is cleared by -inf costs its neighbours few digits.
 //
 // One segment per sequence needs one launch. Longer ones take three: what each segment but the last
 // adds to a state (K and V read once), the states before every segment (a running sum over
 // segments), then the outputs of all segments side by side.
 constexpr int kChunk = 64;
+constexpr float kNone = -104.0f;
 constexpr int kWaveSeqs = 64;   // up to here every wave finds its segment by itself
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -169,10 +171,23 @@ __device__ __forceinline__ u32x4 for_rest(Fp16, u32x4 k)
     return __builtin_bit_cast(u32x4, __builtin_bit_cast(f16x8, k) * (_Float16)(1.0f / 2048.0f));
 }
 
-// Whether either value of the pairs seen is not finite: the exponent field, plus one unit of it,
-// carries into the sign's place. And a pair with zeros in the place of such values.
+// Keeps a branch that is hardly ever taken a branch, rather than selects on the way past it.
+__device__ __forceinline__ void rare() { asm volatile("; rare"); }
+
+// acc plus both values times zero: NaN from the first one on that is not finite.
+__device__ __forceinline__ float times_zero(Bf16, uint32_t w, float acc)
+{
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), bf16x2{(__bf16)0.0f, (__bf16)0.0f}, acc, false);
+}
+__device__ __forceinline__ float times_zero(Fp16, uint32_t w, float acc)
+{
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), f16x2{(_Float16)0.0f, (_Float16)0.0f}, acc, false);
+}
+
+// The sign's place is set for a value that is not finite (its exponent field, plus one unit of it).
 __device__ __forceinline__ uint32_t odd_bits(Bf16, uint32_t w) { return (w & 0x7FFF7FFFu) + 0x00800080u; }
 __device__ __forceinline__ uint32_t odd_bits(Fp16, uint32_t w) { return (w & 0x7FFF7FFFu) + 0x04000400u; }
+// The pair with zeros in the place of such values.
 template <class Type>
 __device__ __forceinline__ uint32_t only_finite(Type t, uint32_t w)
 {
@@ -359,32 +374,51 @@ __global__ __launch_bounds__(kMapThreads) void linear_maps_kernel(LinearArgs a, 
     }
 }
 
+template <int DK, int DV, bool OUT>
+struct ChunkLds {
+    uint16_t k[kChunk][DK + 8];
+    u32x4 v[2][DV / 16][64];                          // second operands: half of the chunk, column
+    u32x4 s[OUT ? DK / 32 : 1][OUT ? DV / 16 : 1][64];   // and the state's: pair of tiles, column
+    float b[kChunk], eb[kChunk], ed[kChunk];          // per token: b (log2), scale e^b, e^(b_63 - b)
+    float grow[DV / 32];                              // a wave's part of s is smaller by this
+    // What is not finite, in even and odd chunks: whether, first token of k, dims of k, first tokens of v
+    uint32_t odd[2], bad_token[2], bad_dims[2][DK / 32], bad_column[2][DV];
+};
+
 // One segment of one head. OUT: its outputs, and the final state where it is the sequence's last;
-// otherwise (segments with a slot) what it adds to the state, and its whole decay.
-template <class Type, int DK, int DV, bool OUT>
-__global__ __launch_bounds__(64 * (DV / 32), 2) void linear_chunk_kernel(LinearArgs a, Cuts cuts)
+// otherwise (segments that are not) what it adds to the state, and its whole decay. REST: the state
+// is kept to the digits of what is returned, or starts others.
+template <class Type, int DK, int DV, bool OUT, bool REST>
+__device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cuts, const Segment &seg,
+                                            ChunkLds<DK, DV, OUT> &lds)
 {
-    constexpr int NW = DV / 32, threads = 64 * NW, EK = DK / 16, WK = EK / 2;
-    constexpr int pieces = DK / 8, loads = kChunk * pieces / threads, stride = DK + 8;
-    constexpr int contractions = DK / 32;
-    __shared__ __align__(16) uint16_t qs[OUT ? kChunk : 1][stride];
-    __shared__ __align__(16) uint16_t ks[kChunk][stride];
-    // per token: b (two floats, log2), scale e^b, e^(b_63 - b)
-    __shared__ __align__(16) float bh[kChunk], bl[kChunk], eb[kChunk], ed[kChunk];
-    __shared__ uint32_t odd_k[NW];   // a wave's part of k holds values that are not finite
+    constexpr int NW = DV / 32, threads = 64 * NW, EK = DK / 16, WK = EK / 2, EV = DV / 16;
+    constexpr int pieces = DK / 8, loads = kChunk * pieces / threads, step = threads / pieces;
+    constexpr int contractions = DK / 32, tiles = OUT ? 4 / NW : 1;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4, h = blockIdx.x;
-    Segment seg;
-    if (!find_segment(a, cuts, blockIdx.y, !OUT, &seg))
-        return;
     const int hk = h / (a.H / a.Hk);
     const uint16_t *qp = (const uint16_t *)a.q + hk * a.hsq, *kp = (const uint16_t *)a.k + hk * a.hsk;
-    const uint16_t *vp = (const uint16_t *)a.v + h * a.hsv + wave * 32 + 2 * col;
+    const uint16_t *vp = (const uint16_t *)a.v + h * a.hsv;
+    uint16_t *op = (uint16_t *)a.out + h * a.hso;
     const float *gp = a.g + h * a.hsg;
-    const int64_t state_at = (int64_t)(4 * g * EK) * DV + wave * 32 + 2 * col;   // of s[0][.][0]
+    const int64_t state_at = (int64_t)(4 * g * EK) * DV + EV * col + 2 * wave;   // of s[0][.][0]
     const int64_t state_size = (int64_t)DK * DV;
+    // This wave's tiles of 16 queries: later ones have more keys, so two waves or work-groups on one SIMD
+    // take them in opposite orders.
+    int tile[tiles];
+    tile[0] = NW == 4 && ((blockIdx.x ^ blockIdx.y) & 1) ? 3 - wave : wave;
+    if constexpr (tiles == 2)
+        tile[1] = 3 - wave;
+    // This wave's share of the v operands: four columns of one half of the chunk.
+    const int v_half = 4 * wave / EV, v_first = 4 * wave % EV;
+    // A lane's part of an address, in bytes; token strides are below 2^24, so it fits 32 bits.
+    const uint32_t row0 = tid / pieces, dim0 = (tid % pieces) * 8;
+    const uint32_t q_lane = 2 * (col * (uint32_t)a.ldq + DK / 4 * g), k_lane = 2 * (row0 * (uint32_t)a.ldk + dim0);
+    const uint32_t v_lane = 2 * (4 * g * (uint32_t)a.ldv + EV * col), o_lane = 2 * (4 * g * (uint32_t)a.ldo + EV * col);
+    const uint32_t g_lane = 4 * lane * (uint32_t)a.ldg;
 
-    // s[j][t][r]: row EK (4g + r) + j, column 32 wave + 2 col + t
+    // s[j][c][r]: row EK (4g + r) + j, column EV col + 2 wave + c
     f32x4 s[EK][2];
     const float *from = nullptr;
     if (OUT && (seg.index > 0 || !seg.last))
@@ -402,44 +436,69 @@ __global__ __launch_bounds__(64 * (DV / 32), 2) void linear_chunk_kernel(LinearA
             s[j][1][r] = x[1];
         }
 
-    u32x4 qn[OUT ? loads : 1], kn[loads];
-    uint32_t vn[16];
+    u32x4 qn[tiles][contractions], kn[loads];
+    u32x2 vn[8];
     float gn = 0.0f;
     auto fetch = [&](int32_t t) {   // a chunk's rows; zeros past the segment's end
         const int32_t n = seg.t1 - t;
-#pragma unroll
-        for (int i = 0; i < loads; ++i) {
-            const int piece = tid + i * threads, row = piece / pieces, d = (piece % pieces) * 8;
-            const int64_t tok = t + min(row, n - 1);
+        const uint16_t *qt = qp + t * a.ldq, *kt = kp + t * a.ldk, *vt = vp + t * a.ldv + v_first;
+        const float *gt = gp + t * a.ldg;
+        if (n >= kChunk) {
             if (OUT)
-                qn[i] = *(const u32x4 *)(qp + tok * a.ldq + d);
-            kn[i] = *(const u32x4 *)(kp + tok * a.ldk + d);
-            if (row >= n) {
-                kn[i] = u32x4{0, 0, 0, 0};
-                if (OUT)
-                    qn[i] = u32x4{0, 0, 0, 0};
-            }
-        }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int row = 32 * (e / 8) + 16 * ((e / 4) & 1) + 4 * g + (e & 3);
-            const int64_t tok = t + min(row, n - 1);
-            vn[e] = *(const uint32_t *)(vp + tok * a.ldv);
-            if (row >= n)
-                vn[e] = 0;
+                for (int i = 0; i < tiles; ++i)
+#pragma unroll
+                    for (int c = 0; c < contractions; ++c)
+                        qn[i][c] = *(const u32x4 *)((const uint8_t *)(qt + 16 * tile[i] * a.ldq + 8 * c) + q_lane);
+#pragma unroll
+            for (int i = 0; i < loads; ++i)
+                kn[i] = *(const u32x4 *)((const uint8_t *)(kt + i * step * a.ldk) + k_lane);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                vn[e] = *(const u32x2 *)(
+                    (const uint8_t *)(vt + (32 * v_half + 16 * (e / 4) + (e & 3)) * a.ldv) + v_lane);
+            gn = *(const float *)((const uint8_t *)gt + g_lane);
+        } else {
+            int own = lane, row_tid = tid;   // opaque: nothing here is worth registers in the loop
+            asm volatile("" : "+v"(own), "+v"(row_tid));
+            if (OUT)
+#pragma unroll
+                for (int i = 0; i < tiles; ++i) {
+                    const int row = 16 * tile[i] + (own & 15), at = min(row, n - 1);
+#pragma unroll
+                    for (int c = 0; c < contractions; ++c)
+                        qn[i][c] = row < n ? *(const u32x4 *)(qt + at * a.ldq + DK / 4 * g + 8 * c) : u32x4{0, 0, 0, 0};
+                }
+#pragma unroll
+            for (int i = 0; i < loads; ++i) {
+                const int row = row_tid / pieces + i * step, at = min(row, n - 1);
+                kn[i] = row < n ? *(const u32x4 *)(kt + at * a.ldk + dim0) : u32x4{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int row = 32 * v_half + 16 * (e / 4) + 4 * (own >> 4) + (e & 3), at = min(row, n - 1);
+                vn[e] = row < n ? *(const u32x2 *)(vt + at * a.ldv + EV * col) : u32x2{0, 0};
+            }
+            gn = lane < n ? gt[min(own, n - 1) * a.ldg] : 0.0f;
         }
-        const int64_t tok = t + min(lane, n - 1);
-        gn = gp[tok * a.ldg];
-        if (lane >= n)
-            gn = 0.0f;
     };
+
+    if (tid < 2) {
+        lds.odd[tid] = 0;
+        lds.bad_token[tid] = kChunk;
+    }
+    if (tid < DK / 16)
+        lds.bad_dims[tid & 1][tid >> 1] = 0;
+    for (int i = tid; i < 2 * DV; i += threads)
+        lds.bad_column[i & 1][i >> 1] = kChunk;
+    bool odd = false;
 
     double whole = 0.0;   // sum of log2 decays of the segment
     if (seg.t0 < seg.t1)
         fetch(seg.t0);
     for (int32_t t = seg.t0; t < seg.t1; t += kChunk) {
         const int32_t n = seg.t1 - t;
-        const float gc = gn < -1.0e4f ? -1.0e4f : gn;
+        const float gc = gn < kNone ? kNone : gn;
         const double b = running_sum((double)gc * 1.44269504088896340736);
         const uint64_t bu = __builtin_bit_cast(uint64_t, b);
         const double end = __builtin_bit_cast(
@@ -447,57 +506,77 @@ __global__ __launch_bounds__(64 * (DV / 32), 2) void linear_chunk_kernel(LinearA
                         (uint32_t)__builtin_amdgcn_readlane((int)bu, 63));
         const float whole_chunk = __builtin_amdgcn_exp2f((float)end);
         whole += end;
+        const int parity = ((t - seg.t0) / kChunk) & 1;
         __syncthreads();   // the previous chunk has been read
-        uint32_t odd = 0;
+
+        // Values of k and v that are not finite (rare) become zeros and mark what they reach: the
+        // outputs of their own and later tokens, their columns or rows of the state. With the matrix
+        // products they would also reach earlier tokens, by way of a zero weight.
+        if (odd) {   // the last chunk's marks have been read
+            rare();
+            if (tid < DK / 32)
+                lds.bad_dims[parity ^ 1][tid] = 0;
+            if (tid == 0) {
+                lds.odd[parity ^ 1] = 0;
+                lds.bad_token[parity ^ 1] = kChunk;
+            }
+            for (int i = tid; i < DV; i += threads)
+                lds.bad_column[parity ^ 1][i] = kChunk;
+        }
+        float seen = 0.0f;   // 0, or NaN where something is not finite
 #pragma unroll
-        for (int i = 0; i < loads; ++i) {
-            const int piece = tid + i * threads, row = piece / pieces, d = (piece % pieces) * 8;
-            if (OUT)
-                *(u32x4 *)&qs[row][d] = qn[i];
-            *(u32x4 *)&ks[row][d] = kn[i];
+        for (int i = 0; i < loads; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                odd |= odd_bits(Type(), kn[i][e]);
-        }
-        odd = __ballot((odd & 0x80008000u) != 0) != 0;
-        if (lane == 0)
-            odd_k[wave] = odd;
-        odd = 0;
+                seen = times_zero(Type(), kn[i][e], seen);
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            odd |= odd_bits(Type(), vn[e]);
-        const bool odd_v = __ballot((odd & 0x80008000u) != 0) != 0;
-        if (wave == 0) {
-            if (OUT) {
-                const float hi = (float)b;
-                bh[lane] = hi;
-                bl[lane] = (float)(b - hi);
-                eb[lane] = a.scale * __builtin_amdgcn_exp2f(hi);
-            }
-            ed[lane] = __builtin_amdgcn_exp2f((float)(end - b));
-        }
-        u32x4 v[2][2];   // [half of the chunk][column parity]: second operands
+        for (int e = 0; e < 8; ++e)
+            seen = times_zero(Type(), vn[e][0], times_zero(Type(), vn[e][1], seen));
+        if (__ballot(seen != seen)) {
+            rare();
+            lds.odd[parity] = 1;
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+            for (int i = 0; i < loads; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t o = odd_bits(Type(), kn[i][e]) & 0x80008000u;
+                    if (o) {
+                        kn[i][e] = only_finite(Type(), kn[i][e]);
+                        const uint32_t d = dim0 + 2 * e;   // even: both dims in one word
+                        atomicMin(&lds.bad_token[parity], row0 + i * step);
+                        atomicOr(&lds.bad_dims[parity][d / 32], ((o >> 15 & 1) | (o >> 30)) << (d % 32));
+                    }
+                }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t o = odd_bits(Type(), vn[e][x]), d = EV * col + v_first + 2 * x;
+                    vn[e][x] = only_finite(Type(), vn[e][x]);
+                    const uint32_t row = 32 * v_half + 16 * (e / 4) + 4 * g + (e & 3);
+                    if (o & 0x8000u)
+                        atomicMin(&lds.bad_column[parity][d], row);
+                    if (o & 0x80000000u)
+                        atomicMin(&lds.bad_column[parity][d + 1], row);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < loads; ++i)
+            *(u32x4 *)&lds.k[row0 + i * step][dim0] = kn[i];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {   // rows paired up: columns v_first + 2x and + 2x + 1
+            u32x4 v0, v1;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint32_t x0 = vn[8 * half + 2 * e], x1 = vn[8 * half + 2 * e + 1];
-                v[half][0][e] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
-                v[half][1][e] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
+                v0[e] = __builtin_amdgcn_perm(vn[2 * e + 1][x], vn[2 * e][x], 0x05040100u);
+                v1[e] = __builtin_amdgcn_perm(vn[2 * e + 1][x], vn[2 * e][x], 0x07060302u);
             }
-        __syncthreads();
-        if (n > kChunk)
-            fetch(t + kChunk);
-        bool odd_any = odd_v;
-#pragma unroll
-        for (int w = 0; w < NW; ++w)
-            odd_any |= odd_k[w] != 0;
-        odd_any = __builtin_amdgcn_readfirstlane(odd_any);
-        __builtin_amdgcn_sched_barrier(0);
-
+            lds.v[v_half][v_first + 2 * x][lane] = v0;
+            lds.v[v_half][v_first + 2 * x + 1][lane] = v1;
+        }
         if (OUT) {
             float most = 0.0f;
-            if constexpr (sizeof(Type) && __is_same(Type, Fp16)) {
+            if constexpr (__is_same(Type, Fp16)) {
 #pragma unroll
                 for (int j = 0; j < EK; ++j)
 #pragma unroll
@@ -506,94 +585,121 @@ __global__ __launch_bounds__(64 * (DV / 32), 2) void linear_chunk_kernel(LinearA
                 for (int d = 1; d < 64; d <<= 1)
                     most = fmaxf(most, __shfl_xor(most, d));
             }
-            const float shrink = fit(Type(), most), grow = 1.0f / shrink;
-            u32x4 sp[WK][2];   // the state as second operands
+            const float shrink = fit(Type(), most);
+            if (__is_same(Type, Fp16) && lane == 0)
+                lds.grow[wave] = 1.0f / shrink;
 #pragma unroll
             for (int p = 0; p < WK; ++p)
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 2; ++c) {
+                    u32x4 x;
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        sp[p][c][r] = pack2(Type(), s[2 * p][c][r] * shrink, s[2 * p + 1][c][r] * shrink);
+                        x[r] = pack2(Type(), s[2 * p][c][r] * shrink, s[2 * p + 1][c][r] * shrink);
+                    lds.s[p][2 * wave + c][lane] = x;
+                }
+        }
+        if (wave == 0) {
+            if (OUT) {
+                lds.b[lane] = (float)b;
+                lds.eb[lane] = a.scale * __builtin_amdgcn_exp2f((float)b);
+            }
+            lds.ed[lane] = __builtin_amdgcn_exp2f((float)(end - b));
+        }
+        u32x4 q[tiles][contractions];   // dims (Dk / 4) g .. + Dk / 4 of token 16 tile + col
+        if (OUT)
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                if (it * 16 >= n)
-                    break;
-                u32x4 q[contractions];   // dims (Dk / 4) g .. + Dk / 4 of token 16 it + col
+            for (int i = 0; i < tiles; ++i)
 #pragma unroll
                 for (int c = 0; c < contractions; ++c)
-                    q[c] = *(const u32x4 *)&qs[16 * it + col][DK / 4 * g + 8 * c];
-                f32x4 o[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+                    q[i][c] = qn[i][c];
+        __syncthreads();
+        if (n > kChunk)
+            fetch(t + kChunk);
+        odd = __builtin_amdgcn_readfirstlane(lds.odd[parity]) != 0;
+        __builtin_amdgcn_sched_barrier(0);
+
+        if (OUT) {
+#pragma unroll
+            for (int i = 0; i < tiles; ++i) {
+                const int it = tile[i];
+                if (it * 16 >= n)
+                    continue;
+                f32x4 o[EV];
+#pragma unroll
+                for (int j = 0; j < EV; ++j)
+                    o[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int p = 0; p < WK; ++p) {
                     u32x4 x;   // words of dims EK r + 2p of the lane's
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        x[r] = q[(WK * r + p) / 4][(WK * r + p) % 4];
-                    o[0] = mfma(Type(), x, sp[p][0], o[0]);
-                    o[1] = mfma(Type(), x, sp[p][1], o[1]);
-                }
-                const f32x4 row = *(const f32x4 *)&eb[16 * it + 4 * g];
+                        x[r] = q[i][(WK * r + p) / 4][(WK * r + p) % 4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    o[0][r] *= row[r] * grow;
-                    o[1][r] *= row[r] * grow;
+                    for (int j = 0; j < EV; ++j)
+                        o[j] = mfma(Type(), x, lds.s[p][j][lane], o[j]);
                 }
-                const float bhi = bh[16 * it + col], blo = bl[16 * it + col];
+                const f32x4 row = *(const f32x4 *)&lds.eb[16 * it + 4 * g];
 #pragma unroll
-                for (int half = 0; half <= it / 2; ++half) {
+                for (int j = 0; j < EV; ++j) {
+                    const float grow = __is_same(Type, Fp16) ? lds.grow[j / 2] : 1.0f;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        o[j][r] *= row[r] * grow;
+                }
+                const float bi = lds.b[16 * it + col];
+                for (int half = 0; 2 * half <= it; ++half) {
                     u32x4 w = {0, 0, 0, 0};   // scores of token 16 it + col with 8 keys of the half
 #pragma unroll
-                    for (int k = 0; k < 2 && 2 * half + k <= it; ++k) {
+                    for (int k = 0; k < 2; ++k) {
                         const int jt = 2 * half + k;
+                        if (jt > it)
+                            break;
                         f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                         for (int c = 0; c < contractions; ++c)
-                            x = mfma(Type(), *(const u32x4 *)&ks[16 * jt + col][DK / 4 * g + 8 * c], q[c], x);
-                        const f32x4 jh = *(const f32x4 *)&bh[16 * jt + 4 * g];
-                        const f32x4 jl = *(const f32x4 *)&bl[16 * jt + 4 * g];
+                            x = mfma(Type(), *(const u32x4 *)&lds.k[16 * jt + col][DK / 4 * g + 8 * c], q[i][c], x);
+                        const f32x4 bj = *(const f32x4 *)&lds.b[16 * jt + 4 * g];
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const float d = __builtin_amdgcn_exp2f((bhi - jh[r]) + (blo - jl[r]));
-                            x[r] = jt < it || 4 * g + r <= col ? x[r] * (a.scale * d) : 0.0f;
+                            x[r] *= a.scale * __builtin_amdgcn_exp2f(bi - bj[r]);
+                            x[r] = jt < it || 4 * g + r <= col ? x[r] : 0.0f;
                         }
                         w[2 * k] = pack2(Type(), x[0], x[1]);
                         w[2 * k + 1] = pack2(Type(), x[2], x[3]);
                     }
-                    if (odd_v && half == it / 2) {
-                        // A later token's infinity must not meet an earlier one's zero weight: each
-                        // token of the tile by itself, with the rows after it cleared.
-                        for (int m = 0; m < 16; ++m)
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                u32x4 x = v[half][c];
+                    for (int j = 0; j < EV; ++j)
+                        o[j] = mfma(Type(), w, lds.v[half][j][lane], o[j]);
+                }
+                if (odd) {
+                    rare();
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int key = 32 * half + 16 * (e / 2) + 4 * g + 2 * (e & 1), i = 16 * it + m;
-                                    x[e] = key > i ? 0u : key + 1 > i ? x[e] & 0xFFFFu : x[e];
-                                }
-                                const f32x4 y = mfma(Type(), w, x, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                    for (int j = 0; j < EV; ++j) {
+                        const uint32_t bad = min(lds.bad_token[parity], lds.bad_column[parity][EV * col + j]);
 #pragma unroll
-                                for (int r = 0; r < 4; ++r)
-                                    if (4 * g + r == m)
-                                        o[c][r] += y[r];
-                            }
-                    } else {
-                        o[0] = mfma(Type(), w, v[half][0], o[0]);
-                        o[1] = mfma(Type(), w, v[half][1], o[1]);
+                        for (int r = 0; r < 4; ++r)
+                            o[j][r] = 16 * it + 4 * g + r >= bad ? NAN : o[j][r];
                     }
                 }
+                uint16_t *ot = op + (t + 16 * it) * a.ldo;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = 16 * it + 4 * g + r;
-                    if (i < n)
-                        *(uint32_t *)((uint16_t *)a.out + (int64_t)(t + i) * a.ldo + h * a.hso + wave * 32 + 2 * col) =
-                            pack2(Type(), o[0][r], o[1][r]);
-                }
+                for (int r = 0; r < 4; ++r)
+                    if (16 * it + 4 * g + r < n) {
+                        uint32_t x[EV / 2];
+#pragma unroll
+                        for (int j = 0; j < EV; j += 2)
+                            x[j / 2] = pack2(Type(), o[j][r], o[j + 1][r]);
+                        uint8_t *to = (uint8_t *)(ot + r * a.ldo) + o_lane;
+                        if constexpr (EV == 8)
+                            *(u32x4 *)to = u32x4{x[0], x[1], x[2], x[3]};
+                        else
+                            *(u32x2 *)to = u32x2{x[0], x[1]};
+                    }
             }
         }
 
-        if (OUT && n <= kChunk && !seg.last)
+        if (OUT && n <= kChunk && !REST)
             break;   // nobody reads the state after this segment
 #pragma unroll
         for (int j = 0; j < EK; ++j)
@@ -602,44 +708,39 @@ __global__ __launch_bounds__(64 * (DV / 32), 2) void linear_chunk_kernel(LinearA
                 s[j][0][r] *= whole_chunk;
                 s[j][1][r] *= whole_chunk;
             }
-        const bool rest = !OUT || seg.last;   // the state is returned, or starts others
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             u32x4 x[2], y[2];   // e^(b_63 - b_j) v_j and what its rounding leaves
 #pragma unroll
+            for (int c = 0; c < 2; ++c)
+                x[c] = lds.v[half][2 * wave + c][lane];
+#pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const f32x2 d = *(const f32x2 *)&ed[32 * half + 16 * (e / 2) + 4 * g + 2 * (e & 1)];
+                const f32x2 d = *(const f32x2 *)&lds.ed[32 * half + 16 * (e / 2) + 4 * g + 2 * (e & 1)];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float v0 = low(Type(), v[half][c][e]) * d[0], v1 = high(Type(), v[half][c][e]) * d[1];
+                    const float v0 = low(Type(), x[c][e]) * d[0], v1 = high(Type(), x[c][e]) * d[1];
                     uint32_t both = pack2(Type(), v0, v1);
-                    // The remainder goes by the bits that the product gets: left to itself, the compiler
-                    // rounds v * d once for one use and twice (float32 first) for the other.
-                    asm volatile("" : "+v"(both));
+                    if (REST) {
+                        // The remainder goes by the bits that the product gets: left to itself, the
+                        // compiler rounds v * d once for one use and twice (float32 first) for the other.
+                        asm volatile("" : "+v"(both));
+                        y[c][e] = rest2(Type(), v0, v1, both);
+                    }
                     x[c][e] = both;
-                    y[c][e] = rest2(Type(), v0, v1, x[c][e]);
                 }
             }
             uint32_t rows[8][WK];   // dims EK col .. of the half's eight keys
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint16_t *p = &ks[32 * half + 16 * (e / 4) + 4 * g + (e & 3)][EK * col];
+                const uint16_t *p = &lds.k[32 * half + 16 * (e / 4) + 4 * g + (e & 3)][EK * col];
                 if constexpr (WK == 4) {
-                    const u32x4 x = *(const u32x4 *)p;
-                    rows[e][0] = x[0]; rows[e][1] = x[1]; rows[e][2] = x[2]; rows[e][3] = x[3];
+                    const u32x4 u = *(const u32x4 *)p;
+                    rows[e][0] = u[0]; rows[e][1] = u[1]; rows[e][2] = u[2]; rows[e][3] = u[3];
                 } else {
-                    const u32x2 x = *(const u32x2 *)p;
-                    rows[e][0] = x[0]; rows[e][1] = x[1];
+                    const u32x2 u = *(const u32x2 *)p;
+                    rows[e][0] = u[0]; rows[e][1] = u[1];
                 }
-            }
-            if (odd_any && rest) {   // an infinity's rounding leaves nothing
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint32_t o = odd_bits(Type(), x[c][e]);
-                        y[c][e] &= (o & 0x8000u ? 0u : 0xFFFFu) | (o & 0x80000000u ? 0u : 0xFFFF0000u);
-                    }
             }
 #pragma unroll
             for (int w = 0; w < WK; ++w) {
@@ -654,14 +755,7 @@ __global__ __launch_bounds__(64 * (DV / 32), 2) void linear_chunk_kernel(LinearA
                     s[2 * w][c] = mfma(Type(), k0, x[c], s[2 * w][c]);
                     s[2 * w + 1][c] = mfma(Type(), k1, x[c], s[2 * w + 1][c]);
                 }
-                if (rest) {
-                    if (odd_any) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            k0[e] = only_finite(Type(), k0[e]);
-                            k1[e] = only_finite(Type(), k1[e]);
-                        }
-                    }
+                if (REST) {
                     k0 = for_rest(Type(), k0);
                     k1 = for_rest(Type(), k1);
 #pragma unroll
@@ -672,9 +766,23 @@ __global__ __launch_bounds__(64 * (DV / 32), 2) void linear_chunk_kernel(LinearA
                 }
             }
         }
+        if (odd) {
+            rare();
+            const bool column0 = lds.bad_column[parity][EV * col + 2 * wave] < kChunk;
+            const bool column1 = lds.bad_column[parity][EV * col + 2 * wave + 1] < kChunk;
+#pragma unroll
+            for (int j = 0; j < EK; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int d = EK * (4 * g + r) + j;
+                    const bool row = lds.bad_dims[parity][d / 32] >> (d % 32) & 1;
+                    s[j][0][r] = row || column0 ? NAN : s[j][0][r];
+                    s[j][1][r] = row || column1 ? NAN : s[j][1][r];
+                }
+        }
     }
 
-    if (OUT && !seg.last)
+    if (OUT && !REST)
         return;
     float *to = OUT ? a.state_out + ((int64_t)seg.seq * a.H + h) * state_size
                     : cuts.states + ((int64_t)(seg.slot + 1) * a.H + h) * state_size;
@@ -685,6 +793,19 @@ __global__ __launch_bounds__(64 * (DV / 32), 2) void linear_chunk_kernel(LinearA
             *(f32x2 *)(to + state_at + (int64_t)(EK * r + j) * DV) = f32x2{s[j][0][r], s[j][1][r]};
     if (!OUT && tid == 0)
         cuts.decays[(int64_t)(seg.slot + 1) * a.H + h] = __builtin_amdgcn_exp2f((float)whole);
+}
+
+template <class Type, int DK, int DV, bool OUT>
+__global__ __launch_bounds__(64 * (DV / 32), 2) void linear_chunk_kernel(LinearArgs a, Cuts cuts)
+{
+    __shared__ __align__(16) ChunkLds<DK, DV, OUT> lds;
+    Segment seg;
+    if (!find_segment(a, cuts, blockIdx.y, !OUT, &seg))
+        return;
+    if (!OUT || seg.last)
+        run_segment<Type, DK, DV, OUT, true>(a, cuts, seg, lds);
+    else
+        run_segment<Type, DK, DV, OUT, false>(a, cuts, seg, lds);
 }
 
 // The state before every segment of a sequence that has several: its slot holds what the segment
