@@ -122,6 +122,7 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 // adds to a state (K and V read once), the states before every segment (a running sum over
 // segments), then the outputs of all segments side by side.
 constexpr int kChunk = 64;
+constexpr int kSegmentThreads = 256;
 constexpr float kNone = -104.0f;
 constexpr int kWaveSeqs = 64;   // up to here every wave finds its segment by itself
 
@@ -170,6 +171,11 @@ __device__ __forceinline__ u32x4 for_rest(Fp16, u32x4 k)
 {
     return __builtin_bit_cast(u32x4, __builtin_bit_cast(f16x8, k) * (_Float16)(1.0f / 2048.0f));
 }
+
+template <int N>
+struct Count {
+    static constexpr int value = N;
+};
 
 // Keeps a branch that is hardly ever taken a branch, rather than selects on the way past it.
 __device__ __forceinline__ void rare() { asm volatile("; rare"); }
@@ -225,9 +231,9 @@ __device__ __forceinline__ double running_sum(double x)
 
 struct Cuts {           // how a call's sequences are cut
     int32_t L;          // tokens per segment, a multiple of kChunk
-    int32_t starts;     // segments that are not their sequence's last, at most
-    int32_t slots;      // states in the workspace: one per segment of a sequence that has several, at most
-    int32_t *maps;      // more than kWaveSeqs sequences: [3][num_seqs + 1] starts, segments, slots before each
+    int32_t inner;      // segments of sequences that have several, at most
+    int32_t slots;      // states in the workspace: one more than segments for each such sequence
+    int32_t *maps;      // more than kWaveSeqs sequences: [3][num_seqs + 1] starts; segments, and inner ones, before each
     float *states;      // [slots][H][Dk][Dv]
     float *decays;      // [slots][H]: a segment's whole decay
 };
@@ -236,10 +242,17 @@ struct Segment {
     int32_t seq, index, last;   // sequence, number inside it, whether it is the sequence's last one
     int32_t t0, t1;             // tokens
     int32_t slot;               // state slot of the segment, where the sequence has several
+    bool single;                // it is the only one of its sequence
 };
 
-// Segment number `unit` of all (inner: of those that are not their sequence's last). A sequence
-// without tokens has one segment. False past the end.
+// Slots before sequence b: its inner segments before, and one for each sequence that has them.
+__device__ __forceinline__ int32_t slot_before(int32_t several, int32_t segments, int32_t b)
+{
+    return several + b - (segments - several);
+}
+
+// Segment number `unit` of all (inner: of those of sequences that have several). A sequence without
+// tokens has one segment. False past the end.
 __device__ bool find_segment(const LinearArgs &a, const Cuts &c, int unit, bool inner, Segment *s)
 {
     int32_t start, end, slot0;
@@ -250,7 +263,7 @@ __device__ bool find_segment(const LinearArgs &a, const Cuts &c, int unit, bool 
         s->index = unit;
         slot0 = 0;
         const int32_t n = max(1, (int32_t)(((int64_t)a.T + c.L - 1) / c.L));
-        if (unit >= n - (inner ? 1 : 0))
+        if (unit >= n || (inner && n == 1))
             return false;
     } else if (a.B <= kWaveSeqs) {
         const int lane = threadIdx.x & 63;
@@ -271,8 +284,9 @@ __device__ bool find_segment(const LinearArgs &a, const Cuts &c, int unit, bool 
         }
         before -= n;
         const uint64_t single = __ballot(n == 1);   // these need no slots
-        const int32_t slots = before - __builtin_popcountll(single & ((1ull << lane) - 1));
-        const int32_t key = inner ? before - min(lane, a.B) : before;
+        const int32_t ones = __builtin_popcountll(single & ((1ull << lane) - 1));
+        const int32_t slots = before - ones + lane - ones;   // segments, and one for each sequence
+        const int32_t key = inner ? before - ones : before;
         const uint64_t hit = __ballot(lane < a.B && key <= unit);
         const int seq = 63 - __builtin_clzll(hit);   // lane 0's key is 0
         s->seq = seq;
@@ -280,16 +294,18 @@ __device__ bool find_segment(const LinearArgs &a, const Cuts &c, int unit, bool 
         end = __builtin_amdgcn_readlane(y, seq);
         s->index = unit - __builtin_amdgcn_readlane(key, seq);
         slot0 = __builtin_amdgcn_readlane(slots, seq);
-        if (s->index >= __builtin_amdgcn_readlane(n, seq) - (inner ? 1 : 0))
+        const int32_t segments = __builtin_amdgcn_readlane(n, seq);
+        if (s->index >= segments || (inner && segments == 1))
             return false;
     } else {
-        const int32_t *starts = c.maps, *segments = starts + a.B + 1, *slots = segments + a.B + 1;
-        if (unit >= segments[a.B] - (inner ? a.B : 0))
+        const int32_t *starts = c.maps, *segments = starts + a.B + 1, *several = segments + a.B + 1;
+        const int32_t *key = inner ? several : segments;
+        if (unit >= key[a.B])
             return false;
         int lo = 0, hi = a.B;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (segments[mid] - (inner ? mid : 0) <= unit)
+            if (key[mid] <= unit)
                 lo = mid;
             else
                 hi = mid;
@@ -297,13 +313,14 @@ __device__ bool find_segment(const LinearArgs &a, const Cuts &c, int unit, bool 
         s->seq = lo;
         start = starts[lo];
         end = max(start, min(max(a.cu[lo + 1], 0), a.T));
-        s->index = unit - (segments[lo] - (inner ? lo : 0));
-        slot0 = slots[lo];
+        s->index = unit - key[lo];
+        slot0 = slot_before(several[lo], segments[lo], lo);
     }
     s->slot = slot0 + s->index;
     s->t0 = (int32_t)min((int64_t)start + (int64_t)s->index * c.L, (int64_t)end);
     s->last = end - s->t0 <= c.L;
     s->t1 = s->last ? end : s->t0 + c.L;
+    s->single = s->last && s->index == 0;
     return true;
 }
 
@@ -313,7 +330,7 @@ __global__ __launch_bounds__(kMapThreads) void linear_maps_kernel(LinearArgs a, 
 {
     __shared__ int32_t wave_x[kMapThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int32_t *starts = c.maps, *segments = starts + a.B + 1, *slots = segments + a.B + 1;
+    int32_t *starts = c.maps, *segments = starts + a.B + 1, *several = segments + a.B + 1;
     __shared__ int32_t wave_one[kMapThreads / 64];
     int32_t top = 0, sum = 0, ones = 0;   // before this round of kMapThreads sequences
     for (int b0 = 0; b0 < a.B; b0 += kMapThreads) {
@@ -365,12 +382,12 @@ __global__ __launch_bounds__(kMapThreads) void linear_maps_kernel(LinearArgs a, 
         if (b < a.B) {
             starts[b] = x;
             segments[b] = s;
-            slots[b] = s - one;   // single segments need none
+            several[b] = s - one;
         }
     }
     if (tid == 0) {
         segments[a.B] = sum;
-        slots[a.B] = sum - ones;
+        several[a.B] = sum - ones;
     }
 }
 
@@ -380,21 +397,23 @@ struct ChunkLds {
     u32x4 v[2][DV / 16][64];                          // second operands: half of the chunk, column
     u32x4 s[OUT ? DK / 32 : 1][OUT ? DV / 16 : 1][64];   // and the state's: pair of tiles, column
     float b[kChunk], eb[kChunk], ed[kChunk];          // per token: b (log2), scale e^b, e^(b_63 - b)
-    float grow[DV / 32];                              // a wave's part of s is smaller by this
+    float grow[kSegmentThreads / 64];                              // a wave's part of s is smaller by this
     // What is not finite, in even and odd chunks: whether, first token of k, dims of k, first tokens of v
     uint32_t odd[2], bad_token[2], bad_dims[2][DK / 32], bad_column[2][DV];
 };
 
-// One segment of one head. OUT: its outputs, and the final state where it is the sequence's last;
-// otherwise (segments that are not) what it adds to the state, and its whole decay. REST: the state
-// is kept to the digits of what is returned, or starts others.
+// One segment of one head. OUT: its outputs, and the final state where it is the sequence's only one;
+// otherwise (inner segments) what it adds to the state, and its whole decay. REST: the state is kept
+// to the digits of what is returned, or starts others. (With a final state from the last one of
+// several as well, those few work-groups alone took 340 us where the others took 230.)
 template <class Type, int DK, int DV, bool OUT, bool REST>
 __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cuts, const Segment &seg,
                                             ChunkLds<DK, DV, OUT> &lds)
 {
-    constexpr int NW = DV / 32, threads = 64 * NW, EK = DK / 16, WK = EK / 2, EV = DV / 16;
+    // a wave owns CW of the EV columns of a lane
+    constexpr int threads = kSegmentThreads, NW = threads / 64, EK = DK / 16, WK = EK / 2, EV = DV / 16, CW = EV / NW;
     constexpr int pieces = DK / 8, loads = kChunk * pieces / threads, step = threads / pieces;
-    constexpr int contractions = DK / 32, tiles = OUT ? 4 / NW : 1;
+    constexpr int contractions = DK / 32;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4, h = blockIdx.x;
     const int hk = h / (a.H / a.Hk);
@@ -402,26 +421,23 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     const uint16_t *vp = (const uint16_t *)a.v + h * a.hsv;
     uint16_t *op = (uint16_t *)a.out + h * a.hso;
     const float *gp = a.g + h * a.hsg;
-    const int64_t state_at = (int64_t)(4 * g * EK) * DV + EV * col + 2 * wave;   // of s[0][.][0]
+    const int64_t state_at = (int64_t)(4 * g * EK) * DV + EV * col + CW * wave;   // of s[0][.][0]
     const int64_t state_size = (int64_t)DK * DV;
-    // This wave's tiles of 16 queries: later ones have more keys, so two waves or work-groups on one SIMD
-    // take them in opposite orders.
-    int tile[tiles];
-    tile[0] = NW == 4 && ((blockIdx.x ^ blockIdx.y) & 1) ? 3 - wave : wave;
-    if constexpr (tiles == 2)
-        tile[1] = 3 - wave;
-    // This wave's share of the v operands: four columns of one half of the chunk.
-    const int v_half = 4 * wave / EV, v_first = 4 * wave % EV;
+    // This wave's tile of 16 queries: later ones have more keys, so work-groups that may share a CU take
+    // them in opposite orders.
+    const int it = (blockIdx.x ^ blockIdx.y) & 1 ? 3 - wave : wave;
+    // This wave's share of the v operands: 2 CW columns of one half of the chunk.
+    const int v_half = 2 * CW * wave / EV, v_first = 2 * CW * wave % EV;
     // A lane's part of an address, in bytes; token strides are below 2^24, so it fits 32 bits.
     const uint32_t row0 = tid / pieces, dim0 = (tid % pieces) * 8;
     const uint32_t q_lane = 2 * (col * (uint32_t)a.ldq + DK / 4 * g), k_lane = 2 * (row0 * (uint32_t)a.ldk + dim0);
     const uint32_t v_lane = 2 * (4 * g * (uint32_t)a.ldv + EV * col), o_lane = 2 * (4 * g * (uint32_t)a.ldo + EV * col);
     const uint32_t g_lane = 4 * lane * (uint32_t)a.ldg;
 
-    // s[j][c][r]: row EK (4g + r) + j, column EV col + 2 wave + c
-    f32x4 s[EK][2];
+    // s[j][c][r]: row EK (4g + r) + j, column EV col + CW wave + c
+    f32x4 s[EK][CW];
     const float *from = nullptr;
-    if (OUT && (seg.index > 0 || !seg.last))
+    if (OUT && !seg.single)
         from = cuts.states + ((int64_t)seg.slot * a.H + h) * state_size + state_at;
     else if (OUT && a.state_in)
         from = a.state_in + ((int64_t)seg.seq * a.H + h) * state_size + state_at;
@@ -429,46 +445,57 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     for (int j = 0; j < EK; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            f32x2 x = {0.0f, 0.0f};
+            float x[CW] = {};
             if (from)
-                x = *(const f32x2 *)(from + (int64_t)(EK * r + j) * DV);
-            s[j][0][r] = x[0];
-            s[j][1][r] = x[1];
+                __builtin_memcpy(x, __builtin_assume_aligned(from + (int64_t)(EK * r + j) * DV, 4 * CW), 4 * CW);
+#pragma unroll
+            for (int c = 0; c < CW; ++c)
+                s[j][c][r] = x[c];
         }
 
-    u32x4 qn[tiles][contractions], kn[loads];
-    u32x2 vn[8];
+    u32x4 q[contractions];   // dims (Dk / 4) g .. + Dk / 4 of token 16 it + col
+    u32x4 kn[loads];
+    typedef uint32_t words __attribute__((ext_vector_type(CW)));
+    words vn[8];
     float gn = 0.0f;
-    auto fetch = [&](int32_t t) {   // a chunk's rows; zeros past the segment's end
+    auto fetch_q = [&](int32_t t) {   // a chunk's rows; zeros past the segment's end
         const int32_t n = seg.t1 - t;
-        const uint16_t *qt = qp + t * a.ldq, *kt = kp + t * a.ldk, *vt = vp + t * a.ldv + v_first;
+        const uint16_t *qt = qp + t * a.ldq;
+        if (n >= kChunk) {
+#pragma unroll
+            for (int c = 0; c < contractions; ++c)
+                q[c] = *(const u32x4 *)((const uint8_t *)(qt + 16 * it * a.ldq + 8 * c) + q_lane);
+        } else {
+            int own = lane;   // opaque: nothing here is worth registers in the loop
+            asm volatile("" : "+v"(own));
+            const int row = 16 * it + (own & 15), at = min(row, n - 1);
+#pragma unroll
+            for (int c = 0; c < contractions; ++c)
+                q[c] = row < n ? *(const u32x4 *)(qt + at * a.ldq + DK / 4 * g + 8 * c) : u32x4{0, 0, 0, 0};
+        }
+    };
+    // The chunk's k, v and decays in `parts` pieces, which are issued between other work: all at once
+    // they would hold up every wave at the same place. A short chunk comes with the first piece.
+    auto fetch = [&](int32_t t, auto parts_type, int part) {
+        constexpr int parts = decltype(parts_type)::value;
+        const int32_t n = seg.t1 - t;
+        const uint16_t *kt = kp + t * a.ldk, *vt = vp + t * a.ldv + v_first;
         const float *gt = gp + t * a.ldg;
         if (n >= kChunk) {
-            if (OUT)
-#pragma unroll
-                for (int i = 0; i < tiles; ++i)
-#pragma unroll
-                    for (int c = 0; c < contractions; ++c)
-                        qn[i][c] = *(const u32x4 *)((const uint8_t *)(qt + 16 * tile[i] * a.ldq + 8 * c) + q_lane);
 #pragma unroll
             for (int i = 0; i < loads; ++i)
-                kn[i] = *(const u32x4 *)((const uint8_t *)(kt + i * step * a.ldk) + k_lane);
+                if (i * parts / loads == part)
+                    kn[i] = *(const u32x4 *)((const uint8_t *)(kt + i * step * a.ldk) + k_lane);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                vn[e] = *(const u32x2 *)(
-                    (const uint8_t *)(vt + (32 * v_half + 16 * (e / 4) + (e & 3)) * a.ldv) + v_lane);
-            gn = *(const float *)((const uint8_t *)gt + g_lane);
-        } else {
-            int own = lane, row_tid = tid;   // opaque: nothing here is worth registers in the loop
+                if (e * parts / 8 == part)
+                    vn[e] = *(const words *)(
+                        (const uint8_t *)(vt + (32 * v_half + 16 * (e / 4) + (e & 3)) * a.ldv) + v_lane);
+            if (part == parts - 1)
+                gn = *(const float *)((const uint8_t *)gt + g_lane);
+        } else if (part == 0 && n > 0) {
+            int own = lane, row_tid = tid;
             asm volatile("" : "+v"(own), "+v"(row_tid));
-            if (OUT)
-#pragma unroll
-                for (int i = 0; i < tiles; ++i) {
-                    const int row = 16 * tile[i] + (own & 15), at = min(row, n - 1);
-#pragma unroll
-                    for (int c = 0; c < contractions; ++c)
-                        qn[i][c] = row < n ? *(const u32x4 *)(qt + at * a.ldq + DK / 4 * g + 8 * c) : u32x4{0, 0, 0, 0};
-                }
 #pragma unroll
             for (int i = 0; i < loads; ++i) {
                 const int row = row_tid / pieces + i * step, at = min(row, n - 1);
@@ -477,7 +504,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int row = 32 * v_half + 16 * (e / 4) + 4 * (own >> 4) + (e & 3), at = min(row, n - 1);
-                vn[e] = row < n ? *(const u32x2 *)(vt + at * a.ldv + EV * col) : u32x2{0, 0};
+                vn[e] = row < n ? *(const words *)(vt + at * a.ldv + EV * col) : words(0);
             }
             gn = lane < n ? gt[min(own, n - 1) * a.ldg] : 0.0f;
         }
@@ -494,8 +521,11 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     bool odd = false;
 
     double whole = 0.0;   // sum of log2 decays of the segment
-    if (seg.t0 < seg.t1)
-        fetch(seg.t0);
+    if (seg.t0 < seg.t1) {
+        fetch(seg.t0, Count<1>(), 0);
+        if (OUT)
+            fetch_q(seg.t0);
+    }
     for (int32_t t = seg.t0; t < seg.t1; t += kChunk) {
         const int32_t n = seg.t1 - t;
         const float gc = gn < kNone ? kNone : gn;
@@ -531,7 +561,9 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                 seen = times_zero(Type(), kn[i][e], seen);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            seen = times_zero(Type(), vn[e][0], times_zero(Type(), vn[e][1], seen));
+#pragma unroll
+            for (int x = 0; x < CW; ++x)
+                seen = times_zero(Type(), vn[e][x], seen);
         if (__ballot(seen != seen)) {
             rare();
             lds.odd[parity] = 1;
@@ -550,7 +582,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
 #pragma unroll
             for (int e = 0; e < 8; ++e)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
+                for (int x = 0; x < CW; ++x) {
                     const uint32_t o = odd_bits(Type(), vn[e][x]), d = EV * col + v_first + 2 * x;
                     vn[e][x] = only_finite(Type(), vn[e][x]);
                     const uint32_t row = 32 * v_half + 16 * (e / 4) + 4 * g + (e & 3);
@@ -564,7 +596,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
         for (int i = 0; i < loads; ++i)
             *(u32x4 *)&lds.k[row0 + i * step][dim0] = kn[i];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {   // rows paired up: columns v_first + 2x and + 2x + 1
+        for (int x = 0; x < CW; ++x) {   // rows paired up: columns v_first + 2x and + 2x + 1
             u32x4 v0, v1;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -581,7 +613,9 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                 for (int j = 0; j < EK; ++j)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        most = fmaxf(most, fmaxf(fabsf(s[j][0][r]), fabsf(s[j][1][r])));
+#pragma unroll
+                        for (int c = 0; c < CW; ++c)
+                            most = fmaxf(most, fabsf(s[j][c][r]));
                 for (int d = 1; d < 64; d <<= 1)
                     most = fmaxf(most, __shfl_xor(most, d));
             }
@@ -591,12 +625,12 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
 #pragma unroll
             for (int p = 0; p < WK; ++p)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < CW; ++c) {
                     u32x4 x;
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         x[r] = pack2(Type(), s[2 * p][c][r] * shrink, s[2 * p + 1][c][r] * shrink);
-                    lds.s[p][2 * wave + c][lane] = x;
+                    lds.s[p][CW * wave + c][lane] = x;
                 }
         }
         if (wave == 0) {
@@ -606,119 +640,110 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             }
             lds.ed[lane] = __builtin_amdgcn_exp2f((float)(end - b));
         }
-        u32x4 q[tiles][contractions];   // dims (Dk / 4) g .. + Dk / 4 of token 16 tile + col
-        if (OUT)
-#pragma unroll
-            for (int i = 0; i < tiles; ++i)
-#pragma unroll
-                for (int c = 0; c < contractions; ++c)
-                    q[i][c] = qn[i][c];
         __syncthreads();
-        if (n > kChunk)
-            fetch(t + kChunk);
         odd = __builtin_amdgcn_readfirstlane(lds.odd[parity]) != 0;
         __builtin_amdgcn_sched_barrier(0);
 
-        if (OUT) {
+        if (OUT && it * 16 < n) {
+            f32x4 o[EV];
 #pragma unroll
-            for (int i = 0; i < tiles; ++i) {
-                const int it = tile[i];
-                if (it * 16 >= n)
-                    continue;
-                f32x4 o[EV];
+            for (int j = 0; j < EV; ++j)
+                o[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < EV; ++j)
-                    o[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int p = 0; p < WK; ++p) {
-                    u32x4 x;   // words of dims EK r + 2p of the lane's
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        x[r] = q[i][(WK * r + p) / 4][(WK * r + p) % 4];
-#pragma unroll
-                    for (int j = 0; j < EV; ++j)
-                        o[j] = mfma(Type(), x, lds.s[p][j][lane], o[j]);
-                }
-                const f32x4 row = *(const f32x4 *)&lds.eb[16 * it + 4 * g];
-#pragma unroll
-                for (int j = 0; j < EV; ++j) {
-                    const float grow = __is_same(Type, Fp16) ? lds.grow[j / 2] : 1.0f;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        o[j][r] *= row[r] * grow;
-                }
-                const float bi = lds.b[16 * it + col];
-                for (int half = 0; 2 * half <= it; ++half) {
-                    u32x4 w = {0, 0, 0, 0};   // scores of token 16 it + col with 8 keys of the half
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int jt = 2 * half + k;
-                        if (jt > it)
-                            break;
-                        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int c = 0; c < contractions; ++c)
-                            x = mfma(Type(), *(const u32x4 *)&lds.k[16 * jt + col][DK / 4 * g + 8 * c], q[i][c], x);
-                        const f32x4 bj = *(const f32x4 *)&lds.b[16 * jt + 4 * g];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            x[r] *= a.scale * __builtin_amdgcn_exp2f(bi - bj[r]);
-                            x[r] = jt < it || 4 * g + r <= col ? x[r] : 0.0f;
-                        }
-                        w[2 * k] = pack2(Type(), x[0], x[1]);
-                        w[2 * k + 1] = pack2(Type(), x[2], x[3]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < EV; ++j)
-                        o[j] = mfma(Type(), w, lds.v[half][j][lane], o[j]);
-                }
-                if (odd) {
-                    rare();
-#pragma unroll
-                    for (int j = 0; j < EV; ++j) {
-                        const uint32_t bad = min(lds.bad_token[parity], lds.bad_column[parity][EV * col + j]);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            o[j][r] = 16 * it + 4 * g + r >= bad ? NAN : o[j][r];
-                    }
-                }
-                uint16_t *ot = op + (t + 16 * it) * a.ldo;
+            for (int p = 0; p < WK; ++p) {
+                fetch(t + kChunk, Count<WK>(), p);
+                __builtin_amdgcn_sched_barrier(0);
+                u32x4 x;   // words of dims EK r + 2p of the lane's
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (16 * it + 4 * g + r < n) {
-                        uint32_t x[EV / 2];
+                    x[r] = q[(WK * r + p) / 4][(WK * r + p) % 4];
 #pragma unroll
-                        for (int j = 0; j < EV; j += 2)
-                            x[j / 2] = pack2(Type(), o[j][r], o[j + 1][r]);
-                        uint8_t *to = (uint8_t *)(ot + r * a.ldo) + o_lane;
-                        if constexpr (EV == 8)
-                            *(u32x4 *)to = u32x4{x[0], x[1], x[2], x[3]};
-                        else
-                            *(u32x2 *)to = u32x2{x[0], x[1]};
-                    }
+                for (int j = 0; j < EV; ++j)
+                    o[j] = mfma(Type(), x, lds.s[p][j][lane], o[j]);
             }
+            const f32x4 row = *(const f32x4 *)&lds.eb[16 * it + 4 * g];
+#pragma unroll
+            for (int j = 0; j < EV; ++j) {
+                const float grow = __is_same(Type, Fp16) ? lds.grow[j / CW] : 1.0f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    o[j][r] *= row[r] * grow;
+            }
+            const float bi = lds.b[16 * it + col];
+            for (int half = 0; 2 * half <= it; ++half) {
+                u32x4 w = {0, 0, 0, 0};   // scores of token 16 it + col with 8 keys of the half
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int jt = 2 * half + k;
+                    if (jt > it)
+                        break;
+                    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int c = 0; c < contractions; ++c)
+                        x = mfma(Type(), *(const u32x4 *)&lds.k[16 * jt + col][DK / 4 * g + 8 * c], q[c], x);
+                    const f32x4 bj = *(const f32x4 *)&lds.b[16 * jt + 4 * g];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        x[r] *= a.scale * __builtin_amdgcn_exp2f(bi - bj[r]);
+                        x[r] = jt < it || 4 * g + r <= col ? x[r] : 0.0f;
+                    }
+                    w[2 * k] = pack2(Type(), x[0], x[1]);
+                    w[2 * k + 1] = pack2(Type(), x[2], x[3]);
+                }
+#pragma unroll
+                for (int j = 0; j < EV; ++j)
+                    o[j] = mfma(Type(), w, lds.v[half][j][lane], o[j]);
+            }
+            if (odd) {
+                rare();
+#pragma unroll
+                for (int j = 0; j < EV; ++j) {
+                    const uint32_t bad = min(lds.bad_token[parity], lds.bad_column[parity][EV * col + j]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        o[j][r] = 16 * it + 4 * g + r >= bad ? NAN : o[j][r];
+                }
+            }
+            uint16_t *ot = op + (t + 16 * it) * a.ldo;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (16 * it + 4 * g + r < n) {
+                    uint32_t x[EV / 2];
+#pragma unroll
+                    for (int j = 0; j < EV; j += 2)
+                        x[j / 2] = pack2(Type(), o[j][r], o[j + 1][r]);
+                    uint8_t *to = (uint8_t *)(ot + r * a.ldo) + o_lane;
+                    if constexpr (EV == 8)
+                        *(u32x4 *)to = u32x4{x[0], x[1], x[2], x[3]};
+                    else
+                        *(u32x2 *)to = u32x2{x[0], x[1]};
+                }
         }
 
         if (OUT && n <= kChunk && !REST)
             break;   // nobody reads the state after this segment
+        if (OUT && n > kChunk)
+            fetch_q(t + kChunk);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < EK; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                s[j][0][r] *= whole_chunk;
-                s[j][1][r] *= whole_chunk;
+#pragma unroll
+                for (int c = 0; c < CW; ++c)
+                    s[j][c][r] *= whole_chunk;
             }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            u32x4 x[2], y[2];   // e^(b_63 - b_j) v_j and what its rounding leaves
+            u32x4 x[CW], y[CW];   // e^(b_63 - b_j) v_j and what its rounding leaves
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                x[c] = lds.v[half][2 * wave + c][lane];
+            for (int c = 0; c < CW; ++c)
+                x[c] = lds.v[half][CW * wave + c][lane];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const f32x2 d = *(const f32x2 *)&lds.ed[32 * half + 16 * (e / 2) + 4 * g + 2 * (e & 1)];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < CW; ++c) {
                     const float v0 = low(Type(), x[c][e]) * d[0], v1 = high(Type(), x[c][e]) * d[1];
                     uint32_t both = pack2(Type(), v0, v1);
                     if (REST) {
@@ -744,6 +769,10 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             }
 #pragma unroll
             for (int w = 0; w < WK; ++w) {
+                if (!OUT) {
+                    fetch(t + kChunk, Count<2 * WK>(), half * WK + w);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
                 u32x4 k0, k1;   // dims EK col + 2w and + 2w + 1
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -751,7 +780,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                     k1[e] = __builtin_amdgcn_perm(rows[2 * e + 1][w], rows[2 * e][w], 0x07060302u);
                 }
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < CW; ++c) {
                     s[2 * w][c] = mfma(Type(), k0, x[c], s[2 * w][c]);
                     s[2 * w + 1][c] = mfma(Type(), k1, x[c], s[2 * w + 1][c]);
                 }
@@ -759,7 +788,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                     k0 = for_rest(Type(), k0);
                     k1 = for_rest(Type(), k1);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < CW; ++c) {
                         s[2 * w][c] = mfma(Type(), k0, y[c], s[2 * w][c]);
                         s[2 * w + 1][c] = mfma(Type(), k1, y[c], s[2 * w + 1][c]);
                     }
@@ -768,17 +797,18 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
         }
         if (odd) {
             rare();
-            const bool column0 = lds.bad_column[parity][EV * col + 2 * wave] < kChunk;
-            const bool column1 = lds.bad_column[parity][EV * col + 2 * wave + 1] < kChunk;
 #pragma unroll
-            for (int j = 0; j < EK; ++j)
+            for (int c = 0; c < CW; ++c) {
+                const bool column = lds.bad_column[parity][EV * col + CW * wave + c] < kChunk;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int d = EK * (4 * g + r) + j;
-                    const bool row = lds.bad_dims[parity][d / 32] >> (d % 32) & 1;
-                    s[j][0][r] = row || column0 ? NAN : s[j][0][r];
-                    s[j][1][r] = row || column1 ? NAN : s[j][1][r];
-                }
+                for (int j = 0; j < EK; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int d = EK * (4 * g + r) + j;
+                        const bool row = lds.bad_dims[parity][d / 32] >> (d % 32) & 1;
+                        s[j][c][r] = row || column ? NAN : s[j][c][r];
+                    }
+            }
         }
     }
 
@@ -789,28 +819,33 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
 #pragma unroll
     for (int j = 0; j < EK; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            *(f32x2 *)(to + state_at + (int64_t)(EK * r + j) * DV) = f32x2{s[j][0][r], s[j][1][r]};
+        for (int r = 0; r < 4; ++r) {
+            float x[CW];
+#pragma unroll
+            for (int c = 0; c < CW; ++c)
+                x[c] = s[j][c][r];
+            __builtin_memcpy(__builtin_assume_aligned(to + state_at + (int64_t)(EK * r + j) * DV, 4 * CW), x, 4 * CW);
+        }
     if (!OUT && tid == 0)
         cuts.decays[(int64_t)(seg.slot + 1) * a.H + h] = __builtin_amdgcn_exp2f((float)whole);
 }
 
 template <class Type, int DK, int DV, bool OUT>
-__global__ __launch_bounds__(64 * (DV / 32), 2) void linear_chunk_kernel(LinearArgs a, Cuts cuts)
+__global__ __launch_bounds__(kSegmentThreads, 2) void linear_chunk_kernel(LinearArgs a, Cuts cuts)
 {
     __shared__ __align__(16) ChunkLds<DK, DV, OUT> lds;
     Segment seg;
     if (!find_segment(a, cuts, blockIdx.y, !OUT, &seg))
         return;
-    if (!OUT || seg.last)
+    if (!OUT || seg.single)
         run_segment<Type, DK, DV, OUT, true>(a, cuts, seg, lds);
     else
         run_segment<Type, DK, DV, OUT, false>(a, cuts, seg, lds);
 }
 
-// The state before every segment of a sequence that has several: its slot holds what the segment
-// before it adds, and then that state (the first one's: state_in, which the sequence's last segment
-// may overwrite). Four elements per thread, the additions of four segments in flight.
+// The state before every segment of a sequence that has several, and the last one: a segment's slot
+// holds what the segment before it adds, and then that state (the first one's: state_in, which may be
+// the same memory as state_out). Four elements per thread, the additions of four segments in flight.
 __global__ __launch_bounds__(256) void linear_states_kernel(LinearArgs a, Cuts c)
 {
     const int32_t size = a.Dk * a.Dv;
@@ -828,12 +863,12 @@ __global__ __launch_bounds__(256) void linear_states_kernel(LinearArgs a, Cuts c
             const int32_t y = max(top, min(max(a.cu[s + 1], 0), a.T));
             n = (int32_t)(((int64_t)(y - top) + c.L - 1) / c.L);
             slot0 = total;
-            total += n > 1 ? n : 0;
+            total += n > 1 ? n + 1 : 0;
         }
     } else {
-        const int32_t *slots = c.maps + 2 * (a.B + 1);
-        slot0 = slots[seq];
-        n = slots[seq + 1] - slot0;
+        const int32_t *segments = c.maps + a.B + 1, *several = segments + a.B + 1;
+        slot0 = slot_before(several[seq], segments[seq], seq);
+        n = several[seq + 1] - several[seq];
     }
     if (n <= 1)
         return;
@@ -846,37 +881,39 @@ __global__ __launch_bounds__(256) void linear_states_kernel(LinearArgs a, Cuts c
         s = *(const f32x4 *)(a.state_in + ((int64_t)seq * a.H + h) * size + at);
     *(f32x4 *)p = s;
     constexpr int U = 4;
-    for (int k = 1; k < n; k += U) {
+    for (int k = 1; k <= n; k += U) {
         f32x4 x[U];
         float f[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (k + u < n) {
+            if (k + u <= n) {
                 x[u] = *(const f32x4 *)(p + (k + u) * step);
                 f[u] = d[(int64_t)(k + u) * a.H];
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (k + u < n) {
+            if (k + u <= n) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     s[e] = fmaf(f[u], s[e], x[u][e]);
-                *(f32x4 *)(p + (k + u) * step) = s;
+                if (k + u < n)
+                    *(f32x4 *)(p + (k + u) * step) = s;
             }
     }
+    *(f32x4 *)(a.state_out + ((int64_t)seq * a.H + h) * size + at) = s;
 }
 
 template <class Type, int DK, int DV>
 hipError_t linear_of(const LinearArgs &a, const Cuts &c, hipStream_t stream)
 {
-    const dim3 block(64 * (DV / 32));
+    const dim3 block(kSegmentThreads);
     if (a.cu && a.B > kWaveSeqs)
         linear_maps_kernel<<<dim3(1), dim3(kMapThreads), 0, stream>>>(a, c);
-    if (c.starts > 0) {
-        linear_chunk_kernel<Type, DK, DV, false><<<dim3(a.H, c.starts), block, 0, stream>>>(a, c);
+    if (c.inner > 0) {
+        linear_chunk_kernel<Type, DK, DV, false><<<dim3(a.H, c.inner), block, 0, stream>>>(a, c);
         linear_states_kernel<<<dim3(a.H, a.B, DK * DV / 1024), dim3(256), 0, stream>>>(a, c);
     }
-    linear_chunk_kernel<Type, DK, DV, true><<<dim3(a.H, c.starts + a.B), block, 0, stream>>>(a, c);
+    linear_chunk_kernel<Type, DK, DV, true><<<dim3(a.H, a.T / c.L + a.B), block, 0, stream>>>(a, c);
     return hipGetLastError();
 }
 
@@ -898,7 +935,7 @@ int32_t segment_length(int32_t T, int32_t H)
         L = 512;
     if (L > 4096)
         L = 4096;
-    while (T / L > 32768)
+    while (T / L > 16384)
         L *= 2;
     return (int32_t)L;
 }
@@ -906,13 +943,14 @@ int32_t segment_length(int32_t T, int32_t H)
 int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
 
 // A sequence of several segments has x + 1 <= 2x of them, x the whole segments before its last token,
-// and all such x sum up to at most T / L.
+// and all such x sum up to at most T / L. One sequence without bounds has T / L and one, if that.
 Cuts cuts_of(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk, int32_t Dv, float *work, int64_t *bytes)
 {
     Cuts c;
     c.L = segment_length(T, H);
-    c.starts = T / c.L;
-    c.slots = 2 * c.starts;
+    const int32_t whole = T / c.L;
+    c.inner = num_seqs == 1 ? whole + (whole > 0) : 2 * whole;
+    c.slots = c.inner + (num_seqs < whole ? num_seqs : whole);
     const int64_t states = (int64_t)c.slots * H * Dk * Dv * 4, decays = round16((int64_t)c.slots * H * 4);
     const int64_t maps = num_seqs > kWaveSeqs ? round16(3 * ((int64_t)num_seqs + 1) * 4) : 0;
     c.states = work;
