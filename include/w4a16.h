@@ -337,7 +337,9 @@ w4a16_status_t w4a16_paged_kv_write(const void *k, int64_t ldk, int64_t hsk, con
  *   (multiples of 8, 16-byte aligned); cache type the same or W4A16_E4M3.
  *   page_table int32[B] rows of row_stride >= max_pages >= 1 entries; seq_lens int32[B];
  *   dim in {64, 96, 128, 192, 256}; Hq % cache->heads == 0, Hq <= 65535; 0 <= B <= 65535;
- *   max_pages * page_size <= 2^31 - 1; window >= 0; scale finite.
+ *   max_pages * page_size <= 2^31 - 1; window >= 0; scale finite; and, for each request and every
+ *   16 query heads of a KV head, the 128-position units that a whole row of its table could have sum up
+ *   to less than 2^31: B * heads * ceil(Hq / heads / 16) * (ceil(max_pages * page_size / 128) + 1).
  *   workspace: w4a16_paged_attention_workspace bytes. Products and sums are held in float32; the
  *   probabilities enter their product with the values rounded to `type`. Repeated calls give
  *   identical bits.

@@ -150,6 +150,9 @@ w4a16_status_t w4a16_paged_attention(const void *q, int64_t ldq, int64_t hsq, in
     if (B < 0 || B > kMaxGrid || need == 0 || max_pages < 1 || row_stride < max_pages || window < 0 ||
         (int64_t)max_pages * cache->page_size > 0x7FFFFFFFLL || !isfinite(scale))
         return W4A16_ERR_BAD_SHAPE;
+    const int64_t share = Hq / cache->heads, units = attention_units(max_pages, cache->page_size);
+    if (units * B > 0x7FFFFFFFLL / (cache->heads * ((share + 15) / 16)))
+        return W4A16_ERR_BAD_SHAPE;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
         !aligned(lse, 4) || !aligned(workspace, 16) || !strided8(ldq, hsq) || !strided8(ldo, hso))
         return W4A16_ERR_MISALIGNED;

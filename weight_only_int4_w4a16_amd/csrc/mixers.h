@@ -63,6 +63,8 @@ hipError_t launch_linear(const LinearArgs &a, int cus, hipStream_t stream);
 hipError_t launch_linear_step(const LinearArgs &a, int cus, hipStream_t stream);
 
 int64_t attention_workspace(int32_t Hq, int32_t heads, int32_t dim);
+// Most units of work of one request and head.
+int64_t attention_units(int32_t max_pages, int32_t page_size);
 int64_t linear_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk, int32_t Dv);
 
 }  // namespace w4a16
