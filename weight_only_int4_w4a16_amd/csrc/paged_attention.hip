@@ -254,10 +254,10 @@ __device__ __forceinline__ void load_part(const uint8_t *p, uint32_t *r)
 {
     constexpr int bytes = E4M3 ? N : 2 * N;
     if constexpr (bytes == 16) {
-        const u32x4 x = *(const u32x4 *)p;
+        const u32x4 x = __builtin_nontemporal_load((const u32x4 *)p);
         r[0] = x[0]; r[1] = x[1]; r[2] = x[2]; r[3] = x[3];
     } else if constexpr (bytes == 8) {
-        const u32x2 x = *(const u32x2 *)p;
+        const u32x2 x = __builtin_nontemporal_load((const u32x2 *)p);
         r[0] = x[0]; r[1] = x[1];
     } else if constexpr (bytes == 4) {
         r[0] = *(const uint32_t *)p;
@@ -313,11 +313,11 @@ struct Keys {   // one half tile: 16 positions
 #pragma unroll
         for (int c = 0; c < chunks; ++c) {
             if constexpr (!E4M3) {
-                const u32x4 x = *(const u32x4 *)(p + 2 * KD::dim(c, g));
+                const u32x4 x = __builtin_nontemporal_load((const u32x4 *)(p + 2 * KD::dim(c, g)));
                 w[c][0] = x[0]; w[c][1] = x[1]; w[c][2] = x[2]; w[c][3] = x[3];
             } else if (c < KD::paired) {
                 if (c % 2 == 0) {
-                    const u32x4 x = *(const u32x4 *)(p + KD::dim(c, g));
+                    const u32x4 x = __builtin_nontemporal_load((const u32x4 *)(p + KD::dim(c, g)));
                     w[c][0] = x[0]; w[c][1] = x[1]; w[c + 1][0] = x[2]; w[c + 1][1] = x[3];
                 }
             } else {

@@ -78,6 +78,14 @@ def _check(status: int, where: str):
 
 def _need(t, name: str, types, ndim: int, dev: int) -> int:
     """Checks one tensor and returns its device's index (`dev` >= 0: the one it has to be on)."""
+    if isinstance(t, torch.Tensor) and t.dtype in types and t.dim() == ndim:
+        at = t.get_device()
+        if at >= 0 and (dev < 0 or at == dev):
+            return at
+    _refuse(t, name, types, ndim, dev)
+
+
+def _refuse(t, name: str, types, ndim: int, dev: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in types:
@@ -87,9 +95,7 @@ def _need(t, name: str, types, ndim: int, dev: int) -> int:
     at = t.get_device()
     if at < 0:
         raise ValueError(f"{name} must be on a GPU")
-    if dev >= 0 and at != dev:
-        raise ValueError(f"{name} is on GPU {at}, the other operands on GPU {dev}")
-    return at
+    raise ValueError(f"{name} is on GPU {at}, the other operands on GPU {dev}")
 
 
 def _flat(t, name: str, types, ndim: int, dev: int) -> int:
@@ -99,9 +105,12 @@ def _flat(t, name: str, types, ndim: int, dev: int) -> int:
     return at
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _guard(dev: int):
     """Makes `dev` the current device for a launch and its allocations where it is not."""
-    return contextlib.nullcontext() if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _HERE if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _handle(stream, dev: int) -> int:
@@ -118,10 +127,11 @@ def _empty(shape, dtype, dev: int, stream):
 
 def _rows(t, name: str):
     """Strides of [rows, heads, dim] with contiguous rows (a dimension of one has none)."""
-    shape, st = t.shape, t.stride()
-    if st[2] != 1 and shape[2] > 1:
+    a, b, c = t.stride()
+    n, m, d = t.shape
+    if c != 1 and d > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
-    return (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0)
+    return (a if n > 1 else 0), (b if m > 1 else 0)
 
 
 def _cache_of(k_cache, v_cache, k_scale, v_scale, kind, dev: int) -> _Cache:
@@ -221,7 +231,7 @@ def paged_kv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     _flat(slot_map, "slot_map", _I32, 1, dev)
     c = _cache_of(k_cache, v_cache, k_scale, v_scale, k.dtype, dev)
     T = slot_map.shape[0]
-    if k.shape != v.shape or tuple(k.shape) != (T, c.heads, c.dim):
+    if k.shape != v.shape or k.shape != (T, c.heads, c.dim):
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must be [{T}, {c.heads}, {c.dim}]")
     ldk, hsk = _rows(k, "k")
     ldv, hsv = _rows(v, "v")
@@ -282,7 +292,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         ldo, hso = _rows(out, "out")
         if lse is not None:
             _flat(lse, "lse", _F32, 2, dev)
-            if tuple(lse.shape) != (B, Hq):
+            if lse.shape != (B, Hq):
                 raise ValueError(f"lse must be {(B, Hq)}, got {tuple(lse.shape)}")
         workspace, at, room = _scratch(
             workspace, lib.w4a16_paged_attention_workspace(Hq, c.heads, dim) if workspace is None else 0,
@@ -309,7 +319,7 @@ def _mixer(q, k, v, log_decay, dev_first: int = -1):
         raise TypeError("log_decay must be a torch.Tensor")
     per_token = log_decay.dim() == 2
     _need(log_decay, "log_decay", _F32, 2 if per_token else 1, dev)
-    if tuple(log_decay.shape) != ((T, H) if per_token else (H,)):
+    if log_decay.shape != ((T, H) if per_token else (H,)):
         raise ValueError(f"log_decay must be [{H}] or [{T}, {H}], got {tuple(log_decay.shape)}")
     st = log_decay.stride()
     return dev, T, Hk, H, Dk, Dv, (st[0] if per_token else 0), st[-1]
@@ -317,7 +327,7 @@ def _mixer(q, k, v, log_decay, dev_first: int = -1):
 
 def _state(t, name: str, rows: int, H: int, Dk: int, Dv: int, dev: int):
     _flat(t, name, _F32, 4, dev)
-    if tuple(t.shape) != (rows, H, Dk, Dv):
+    if t.shape != (rows, H, Dk, Dv):
         raise ValueError(f"{name} must be {(rows, H, Dk, Dv)}, got {tuple(t.shape)}")
 
 
