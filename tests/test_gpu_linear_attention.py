@@ -113,6 +113,51 @@ def test_small_and_large_magnitudes():
     x.check(*x.run())
 
 
+@pytest.mark.parametrize("dtype,Dk,Dv", [(torch.bfloat16, 128, 128), (torch.float16, 64, 128), (torch.bfloat16, 128, 64)])
+def test_infinities_and_nan_reach_later_tokens_only(dtype, Dk, Dv):
+    """A value that is not finite makes outputs of its own and later tokens not finite, and the parts of
+    the state that it enters; all that comes before it, other columns of v and other heads keep their values."""
+    n, H = 200, 2
+    clean = Linear([n, 70], H, H, Dk, Dv, dtype, seed=30)
+    want, state = clean.run()
+    for name, t, h, d, value in (("v", 100, 0, 5, math.inf), ("v", 63, 1, Dv - 1, math.nan), ("v", 0, 0, 0, -math.inf),
+                                 ("k", 77, 0, 9, math.nan), ("k", 128, 1, Dk - 1, math.inf), ("q", 90, 0, 3, math.nan)):
+        x = Linear([n, 70], H, H, Dk, Dv, dtype, seed=30)
+        getattr(x, name)[t, h, d] = value
+        out, got = x.run()
+        bad = torch.zeros(want.shape, dtype=torch.bool)
+        bad_state = torch.zeros(state.shape, dtype=torch.bool)
+        if name == "v":
+            bad[t:n, h, d] = True
+            bad_state[0, h, :, d] = True
+        elif name == "k":
+            bad[t:n, h] = True
+            bad_state[0, h, d] = True
+        else:
+            bad[t, h] = True
+        assert torch.equal(~out.cpu().isfinite(), bad), (name, t)
+        assert torch.equal(~got.cpu().isfinite(), bad_state), (name, t)
+        # the others: the same sums but for what stood in the value's place, so within two bounds
+        x2 = Linear([n, 70], H, H, Dk, Dv, dtype, seed=30)
+        getattr(x2, name)[t, h, d] = 0.0
+        ref, ref_state = x2.run()
+        scale = float(want.float().abs().max())
+        off = (out.float() - ref.float()).cpu()[~bad].abs().max()
+        assert float(off) <= 4 * mo.half_step(dtype) * scale, (name, t)
+        off = (got - ref_state).cpu()[~bad_state].abs().max()
+        assert float(off) <= 2.0 ** -15 * float(ref_state.abs().max()), (name, t)
+
+
+def test_step_keeps_infinities_to_their_columns():
+    x = Linear([1] * 3, 2, 2, 64, 64, seed=31)
+    x.v[1, 0, 7] = math.inf
+    q, k, v, g, s = (t.cuda() for t in (x.q, x.k, x.v, x.g, x.state))
+    out = w.linear_attention_step(q, k, v, g, s)
+    bad = torch.zeros(3, 2, 64, dtype=torch.bool)
+    bad[1, 0, 7] = True
+    assert torch.equal(~out.cpu().isfinite(), bad)
+
+
 def test_tokens_outside_sequences_are_left_alone():
     x = Linear([40, 60], 2, 2, 64, 64, seed=8, lead=5)
     extra = torch.full((105, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
@@ -123,6 +168,27 @@ def test_tokens_outside_sequences_are_left_alone():
     # decreasing and out-of-range values are clamped: sequences of 30, 0 and 75 tokens
     x = Linear([30, 0, 75], 2, 2, 64, 64, seed=9)
     x.check(*x.run(cu_seqlens=ints([-4, 30, 10, 2 ** 31 - 1])))
+
+
+def test_many_and_long_sequences_share_segments():
+    """More sequences than a wave holds, some of them cut into segments."""
+    gen = torch.Generator().manual_seed(2)
+    lens = torch.randint(0, 4, (80,), generator=gen).tolist()
+    lens[3], lens[40], lens[79] = 1300, 700, 513
+    x = Linear(lens, 1, 1, 64, 64, seed=32, rate=0.02)
+    out, state = x.run()
+    x.check(out, state)
+    few = Linear([0, 1300, 2, 700, 0, 513, 512, 1], 2, 1, 64, 128, torch.float16, seed=33, rate=0.02)
+    few.check(*few.run())
+
+
+def test_in_place_state_of_several_segments():
+    x = Linear([1400], 2, 2, 64, 64, seed=34, rate=0.01)
+    state = x.state.cuda()
+    out, got = x.run(state=state, state_out=state)
+    x.check(out, got)
+    again, _ = x.run()
+    assert torch.equal(out, again)
 
 
 def test_many_sequences():
