@@ -371,7 +371,8 @@ int64_t w4a16_paged_attention_workspace(int32_t Hq, int32_t heads, int32_t dim);
  *   (a sequence without tokens gets its state_in); state_out == state_in is allowed.
  *   Dk, Dv in {64, 128}; H % Hk == 0; 0 <= T <= 2^31 - 65; 1 <= num_seqs <= 16384; H <= 32767.
  *   States, decays and sums are held in float32 or more; within the library the operands of matrix
- *   products are rounded to `type`, those that reach state_out as a sum of two such values.
+ *   products are rounded to `type`, those that reach state_out as a sum of such values (24 bits of
+ *   three bfloat16, 22 of two float16).
  */
 w4a16_status_t w4a16_linear_attention(const void *q, int64_t ldq, int64_t hsq, const void *k,
                                       int64_t ldk, int64_t hsk, const void *v, int64_t ldv,

@@ -126,8 +126,8 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 //   first operand, q at dk = EK (4g + r) + {j, j + 1}, are words that the lane has loaded for the scores.
 //
 // Roundings: scores with their decay, S in q S, and e^{b_63 - b_j} v_j are rounded to the type for
-// their products, the last one kept as a sum of two values where the result reaches a returned
-// state. Decays are summed in float64 over a chunk; the scores' take the sums in float32, off by 2^-24
+// their products, the last one kept as a sum of three bfloat16 or two float16 values (24 and 22 bits) where
+// the result reaches a returned state. Decays are summed in float64 over a chunk; the scores' take the sums in float32, off by 2^-24
 // of their size. A log decay below -104 counts as that: e^-104 is zero in float32, and so a state that
 // is cleared by -inf costs its neighbours few digits.
 //
@@ -169,16 +169,27 @@ __device__ __forceinline__ float high(Bf16, uint32_t w) { return __builtin_bit_c
 __device__ __forceinline__ float low(Fp16, uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[0]; }
 __device__ __forceinline__ float high(Fp16, uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[1]; }
 
-// What is left of (a, b) after rounding to the packed pair `w`. A float16 remainder is kept 2^11 times
-// as large, so that it does not fall among the subnormals, and meets k times 2^-11.
-__device__ __forceinline__ uint32_t rest2(Bf16 t, float a, float b, uint32_t w)
+// What rounding to `r` leaves of x. A float16 remainder is kept 2^11 times as large, so that it does not
+// fall among the subnormals, and meets k times 2^-11.
+__device__ __forceinline__ float left(Bf16, float x, float r) { return x - r; }
+__device__ __forceinline__ float left(Fp16, float x, float r) { return (x - r) * 2048.0f; }
+// Rounds a pair and keeps what that leaves in its place, for the next term. The remainder goes by the bits
+// that the product gets: left to itself, the compiler rounds v * d once for one use and twice (float32
+// first) for the other.
+template <class Type>
+__device__ __forceinline__ uint32_t take(Type t, float &a, float &b)
 {
-    return pack2(t, a - low(t, w), b - high(t, w));
+    uint32_t both = pack2(t, a, b);
+    asm volatile("" : "+v"(both));
+    a = left(t, a, low(t, both));
+    b = left(t, b, high(t, both));
+    return both;
 }
-__device__ __forceinline__ uint32_t rest2(Fp16 t, float a, float b, uint32_t w)
-{
-    return pack2(t, (a - low(t, w)) * 2048.0f, (b - high(t, w)) * 2048.0f);
-}
+// As many values of the type as hold a float32's digits.
+template <class Type>
+struct Terms {
+    static constexpr int count = __is_same(Type, Bf16) ? 3 : 2;
+};
 __device__ __forceinline__ u32x4 for_rest(Bf16, u32x4 k) { return k; }
 __device__ __forceinline__ u32x4 for_rest(Fp16, u32x4 k)
 {
@@ -748,24 +759,20 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            u32x4 x[CW], y[CW];   // e^(b_63 - b_j) v_j and what its rounding leaves
+            constexpr int terms = REST ? Terms<Type>::count : 1;
+            u32x4 x[terms][CW];   // e^(b_63 - b_j) v_j, rounded, and what the rounding leaves
 #pragma unroll
             for (int c = 0; c < CW; ++c)
-                x[c] = lds.v[half][CW * wave + c][lane];
+                x[0][c] = lds.v[half][CW * wave + c][lane];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const f32x2 d = *(const f32x2 *)&lds.ed[32 * half + 16 * (e / 2) + 4 * g + 2 * (e & 1)];
 #pragma unroll
                 for (int c = 0; c < CW; ++c) {
-                    const float v0 = low(Type(), x[c][e]) * d[0], v1 = high(Type(), x[c][e]) * d[1];
-                    uint32_t both = pack2(Type(), v0, v1);
-                    if (REST) {
-                        // The remainder goes by the bits that the product gets: left to itself, the
-                        // compiler rounds v * d once for one use and twice (float32 first) for the other.
-                        asm volatile("" : "+v"(both));
-                        y[c][e] = rest2(Type(), v0, v1, both);
-                    }
-                    x[c][e] = both;
+                    float v0 = low(Type(), x[0][c][e]) * d[0], v1 = high(Type(), x[0][c][e]) * d[1];
+#pragma unroll
+                    for (int i = 0; i < terms; ++i)
+                        x[i][c][e] = take(Type(), v0, v1);
                 }
             }
             uint32_t rows[8][WK];   // dims EK col .. of the half's eight keys
@@ -793,17 +800,15 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                     k1[e] = __builtin_amdgcn_perm(rows[2 * e + 1][w], rows[2 * e][w], 0x07060302u);
                 }
 #pragma unroll
-                for (int c = 0; c < CW; ++c) {
-                    s[2 * w][c] = mfma(Type(), k0, x[c], s[2 * w][c]);
-                    s[2 * w + 1][c] = mfma(Type(), k1, x[c], s[2 * w + 1][c]);
-                }
-                if (REST) {
-                    k0 = for_rest(Type(), k0);
-                    k1 = for_rest(Type(), k1);
+                for (int i = 0; i < terms; ++i) {
+                    if (i == 1) {
+                        k0 = for_rest(Type(), k0);
+                        k1 = for_rest(Type(), k1);
+                    }
 #pragma unroll
                     for (int c = 0; c < CW; ++c) {
-                        s[2 * w][c] = mfma(Type(), k0, y[c], s[2 * w][c]);
-                        s[2 * w + 1][c] = mfma(Type(), k1, y[c], s[2 * w + 1][c]);
+                        s[2 * w][c] = mfma(Type(), k0, x[i][c], s[2 * w][c]);
+                        s[2 * w + 1][c] = mfma(Type(), k1, x[i][c], s[2 * w + 1][c]);
                     }
                 }
             }
