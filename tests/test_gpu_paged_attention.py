@@ -239,3 +239,31 @@ def test_empty_batch_and_refusals():
     with pytest.raises(w.W4A16Error, match="workspace"):
         w.paged_attention(p.q.cuda(), p.k, p.v, ints(p.table), ints([5]),
                           workspace=torch.empty(0, dtype=torch.uint8, device="cuda").new_empty(8))
+
+
+def test_short_way_refuses_like_the_long_one():
+    """With outputs and scratch given, calls go through the C++ binding: same results, same refusals."""
+    p = Paged([90, 3], 4, 2, 64, 16, torch.float16, True, "nhd", seed=11)
+    q, table, lens = p.q.cuda(), ints(p.table), ints(p.lens)
+    out, work = torch.empty_like(q), w.paged_attention_workspace(q, p.k)
+    ks, vs = (s.cuda() for s in p.scales)
+
+    def call(**kw):
+        a = dict(q=q, k_cache=p.k, v_cache=p.v, page_table=table, seq_lens=lens, scale=0.125, k_scale=ks, v_scale=vs,
+                 out=out, workspace=work)
+        a.update(kw)
+        return w.paged_attention(**a)
+
+    p.check(call(), None, 0.125)
+    long, _ = p.run(0.125, lse=False)
+    assert torch.equal(long, out)
+    assert torch.equal(call(scale=None), call(scale=64 ** -0.5))
+    for kw, kind, text in (
+            (dict(seq_lens=lens.long()), TypeError, "seq_lens"), (dict(seq_lens=lens[:1]), ValueError, "mismatch"),
+            (dict(q=q.float()), TypeError, "q must"), (dict(out=out[:1]), ValueError, "out must"),
+            (dict(k_scale=ks[:1]), ValueError, "one value"), (dict(v_cache=p.v[..., :32]), ValueError, "differ"),
+            (dict(workspace=work[:100]), w.W4A16Error, "workspace"), (dict(window=-1), w.W4A16Error, "shape"),
+            (dict(page_table=table.cpu()), ValueError, "GPU"), (dict(out=out.transpose(1, 2).contiguous().transpose(1, 2)),
+                                                                ValueError, "unit stride")):
+        with pytest.raises(kind, match=text):
+            call(**kw)

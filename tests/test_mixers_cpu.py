@@ -199,3 +199,25 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         w.linear_attention(None, q, q, ints.float())
     with pytest.raises(TypeError, match="ctx_lens"):
         w.page_tables(ints.long(), ints, ints[None], ints, 16, max_tokens=4)
+
+
+def test_short_way_declines_what_it_does_not_take():
+    """The C++ part of the binding leaves everything but plain GPU calls to the Python code."""
+    mixers._library()
+    b = mixers._binding
+    x = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    c = torch.zeros(1, 16, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    work = torch.zeros(16, dtype=torch.uint8)
+    assert b.page_tables(i, i, i[None], i, 16, i, i, i, i, i) == -1
+    assert b.page_tables(i, i, i[None], i, "16", i, i, i, i, i) == -1
+    assert b.paged_kv_write(x, x, c, c, None, None, i) == -1
+    assert b.paged_attention(x, c, c, None, None, i[None], i, 1.0, 0, x, None, work) == -1
+    assert b.paged_attention(None, c, c, None, None, i[None], i, None, 0, x, None, work) == -1
+    assert b.linear_attention(x, x, x, i.float(), None, None, x, 1.0, x, work) == -1
+    assert b.linear_attention_step(x, x, x, i.float(), x, None, x, 1.0, x) == -1
+    assert b.paged_kv_write(x) == -1 and b.linear_attention_step() == -1
+    with pytest.raises(TypeError):
+        b.bind(1, 2)
+    with pytest.raises(ValueError):
+        b.bind(0, 1, 2, 3, 4)

@@ -1,8 +1,10 @@
 """Token mixers of a decode or prompt step: page tables, the paged key-value cache, attention of one
 new token over it, and linear attention with a decay for each head.
 
-Like the rest of the package this is a thin ctypes binding: it checks and marshals arguments, and
-every step of the computation runs in the HIP kernels of libw4a16.so. There is no fallback.
+Like the rest of the package this only checks and marshals arguments; every step of the computation
+runs in the HIP kernels of libw4a16.so, and there is no fallback. Calls whose outputs and scratch are
+given, on the current device and stream, go through _binding (C++, a few microseconds less per call);
+all others, and all refusals, through the code below.
 
 Tensor conventions:
   caches      [pages, page_size, heads, dim], unit stride along dim, other strides free (a
@@ -42,14 +44,23 @@ class _Cache(ctypes.Structure):
 
 _Strides = _i64 * 3
 _lib = None
+_binding = None
 
 
 def _library():
-    """libw4a16.so with the argument types of this module's entry points."""
-    global _lib
+    """libw4a16.so with the argument types of this module's entry points; loads _binding as well."""
+    global _lib, _binding
     if _lib is None:
         from . import library
         lib = library()
+        try:
+            from . import _binding as binding
+        except ImportError as e:
+            raise ImportError("_binding.so is missing or does not load: build it with "
+                              "`python -m weight_only_int4_w4a16_amd.build`") from e
+        _binding = binding
+        _binding.bind(*[ctypes.cast(getattr(lib, "w4a16_" + n), _P).value for n in (
+            "page_tables", "paged_kv_write", "paged_attention", "linear_attention", "linear_attention_step")])
         row = [_P, _i64, _i64]
         lib.w4a16_page_tables.argtypes = [_P, _P, _i32, _P, _i64, _i32, _P, _i32, _i32, _i32,
                                           _P, _P, _P, _P, _P, _P]
@@ -106,6 +117,20 @@ def _flat(t, name: str, types, ndim: int, dev: int) -> int:
 
 
 _HERE = contextlib.nullcontext()
+
+
+def _short(status: int, where: str) -> bool:
+    """Whether the short way took a call: raises for a refusal of the C entry."""
+    if status > 0:
+        _check(status, where)
+    return status == 0
+
+
+def _factor(scale, t):
+    """scale, or the default for rows like t's; None where neither can be told."""
+    if scale is None and isinstance(t, torch.Tensor) and t.dim() == 3 and t.shape[2]:
+        return t.shape[2] ** -0.5
+    return scale
 
 
 def _guard(dev: int):
@@ -188,6 +213,11 @@ def page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, page_table: torc
     requests one after the other: the lengths after the step, the requests' first tokens, each
     token's slot and position (-1 past the last token, slot -1 where there is no page), and the
     counts of tokens and pages taken. Give max_tokens or `out`."""
+    if out is not None and max_tokens is None and stream is None:
+        _library()
+        if _short(_binding.page_tables(ctx_lens, new_lens, page_table, free_pages, page_size, *out),
+                  "w4a16_page_tables"):
+            return out
     dev = _flat(ctx_lens, "ctx_lens", _I32, 1, -1)
     _flat(new_lens, "new_lens", _I32, 1, dev)
     _need(page_table, "page_table", _I32, 2, dev)
@@ -226,6 +256,11 @@ def paged_kv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     """Writes k and v [T, heads, dim] (bfloat16 or float16) to the slots slot_map int32 [T] of a paged
     cache of the same type, or of float8_e4m3fn after division by the head's scale (saturating, to
     nearest even). Tokens whose slot is outside the cache are skipped."""
+    if stream is None:
+        _library()
+        if _short(_binding.paged_kv_write(k, v, k_cache, v_cache, k_scale, v_scale, slot_map),
+                  "w4a16_paged_kv_write"):
+            return
     dev = _need(k, "k", _HALF, 3, -1)
     _need(v, "v", (k.dtype,), 3, dev)
     _flat(slot_map, "slot_map", _I32, 1, dev)
@@ -269,6 +304,12 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     defaults to dim ** -0.5. Returns out, like q; lse, float32 [B, Hq], receives log sum exp of the scores.
     A request of length 0 gets zeros and -inf. `workspace` (paged_attention_workspace) may be kept
     for all calls on one stream."""
+    if out is not None and workspace is not None and stream is None:
+        _library()
+        if _short(_binding.paged_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens,
+                                           _factor(scale, q), window, out, lse, workspace),
+                  "w4a16_paged_attention"):
+            return out
     dev = _need(q, "q", _HALF, 3, -1)
     c = _cache_of(k_cache, v_cache, k_scale, v_scale, q.dtype, dev)
     _need(page_table, "page_table", _I32, 2, dev)
@@ -359,6 +400,11 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     log_decay float32 [T, H], or [H] for decays fixed for each head; cu_seqlens int32 [num_seqs + 1] on the
     GPU, or None for one sequence; state float32 [num_seqs, H, Dk, Dv], or None for zeros. scale defaults
     to Dk ** -0.5. Returns (out [T, H, Dv], state_out), where state_out may be `state` itself."""
+    if out is not None and state_out is not None and workspace is not None and stream is None:
+        _library()
+        if _short(_binding.linear_attention(q, k, v, log_decay, cu_seqlens, state, state_out,
+                                            _factor(scale, q), out, workspace), "w4a16_linear_attention"):
+            return out, state_out
     dev, T, Hk, H, Dk, Dv, ldg, hsg = _mixer(q, k, v, log_decay)
     seqs = 1
     if cu_seqlens is not None:
@@ -395,6 +441,12 @@ def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log
     log_decay [B, H] or [H]. state float32 [num_states, H, Dk, Dv] is updated in place unless state_out is
     given; request b's state is row slots[b] (int32 [B], all different; outside the pool: a zero row and
     no state) or, without slots, row b. Returns out [B, H, Dv]."""
+    if out is not None and stream is None:
+        _library()
+        if _short(_binding.linear_attention_step(q, k, v, log_decay, state, slots,
+                                                 state if state_out is None else state_out,
+                                                 _factor(scale, q), out), "w4a16_linear_attention_step"):
+            return out
     dev, B, Hk, H, Dk, Dv, ldg, hsg = _mixer(q, k, v, log_decay)
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be a [num_states, H, Dk, Dv] tensor")
