@@ -275,6 +275,42 @@ __device__ __forceinline__ int32_t slot_before(int32_t several, int32_t segments
     return several + b - (segments - several);
 }
 
+// One sequence per lane, kWaveSeqs of them at most: its tokens, its segments, those of the sequences
+// before it, and how many of these have one segment only and need no slots.
+struct LaneCut {
+    int32_t start, end, n, before, ones;
+};
+
+__device__ __forceinline__ LaneCut lane_cut(const LinearArgs &a, const Cuts &c)
+{
+    const int lane = threadIdx.x & 63;
+    const int at = min(lane, a.B);
+    LaneCut s;
+    s.start = min(max(a.cu[at], 0), a.T);
+    s.end = min(max(a.cu[min(at + 1, a.B)], 0), a.T);
+    for (int d = 1; d < 64; d <<= 1) {   // running maximum of the starts
+        const int32_t o = __shfl_up(s.start, d);
+        if (lane >= d)
+            s.start = max(s.start, o);
+    }
+    s.end = max(s.start, s.end);
+    s.n = lane < a.B ? max(1, (int32_t)(((int64_t)(s.end - s.start) + c.L - 1) / c.L)) : 0;
+    const uint64_t single = __ballot(s.n == 1);
+    s.ones = __builtin_popcountll(single & ((1ull << lane) - 1));
+    s.before = s.n;
+    if (__ballot(s.n > 1)) {
+        for (int d = 1; d < 64; d <<= 1) {
+            const int32_t o = __shfl_up(s.before, d);
+            if (lane >= d)
+                s.before += o;
+        }
+        s.before -= s.n;
+    } else {   // one each
+        s.before = lane;
+    }
+    return s;
+}
+
 // Segment number `unit` of all (inner: of those of sequences that have several). A sequence without
 // tokens has one segment. False past the end.
 __device__ bool find_segment(const LinearArgs &a, const Cuts &c, int unit, bool inner, Segment *s)
@@ -291,34 +327,16 @@ __device__ bool find_segment(const LinearArgs &a, const Cuts &c, int unit, bool 
             return false;
     } else if (a.B <= kWaveSeqs) {
         const int lane = threadIdx.x & 63;
-        const int at = min(lane, a.B);
-        int32_t x = min(max(a.cu[at], 0), a.T), y = min(max(a.cu[min(at + 1, a.B)], 0), a.T);
-        for (int d = 1; d < 64; d <<= 1) {   // running maximum of the starts
-            const int32_t o = __shfl_up(x, d);
-            if (lane >= d)
-                x = max(x, o);
-        }
-        y = max(x, y);
-        const int32_t n = lane < a.B ? max(1, (int32_t)(((int64_t)(y - x) + c.L - 1) / c.L)) : 0;
-        int32_t before = n;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int32_t o = __shfl_up(before, d);
-            if (lane >= d)
-                before += o;
-        }
-        before -= n;
-        const uint64_t single = __ballot(n == 1);   // these need no slots
-        const int32_t ones = __builtin_popcountll(single & ((1ull << lane) - 1));
-        const int32_t slots = before - ones + lane - ones;   // segments, and one for each sequence
-        const int32_t key = inner ? before - ones : before;
+        const LaneCut cut = lane_cut(a, c);
+        const int32_t key = inner ? cut.before - cut.ones : cut.before;
         const uint64_t hit = __ballot(lane < a.B && key <= unit);
         const int seq = 63 - __builtin_clzll(hit);   // lane 0's key is 0
         s->seq = seq;
-        start = __builtin_amdgcn_readlane(x, seq);
-        end = __builtin_amdgcn_readlane(y, seq);
+        start = __builtin_amdgcn_readlane(cut.start, seq);
+        end = __builtin_amdgcn_readlane(cut.end, seq);
         s->index = unit - __builtin_amdgcn_readlane(key, seq);
-        slot0 = __builtin_amdgcn_readlane(slots, seq);
-        const int32_t segments = __builtin_amdgcn_readlane(n, seq);
+        slot0 = __builtin_amdgcn_readlane(slot_before(cut.before - cut.ones, cut.before, lane), seq);
+        const int32_t segments = __builtin_amdgcn_readlane(cut.n, seq);
         if (s->index >= segments || (inner && segments == 1))
             return false;
     } else {
@@ -874,15 +892,9 @@ __global__ __launch_bounds__(256) void linear_states_kernel(LinearArgs a, Cuts c
         slot0 = 0;
         n = (int32_t)(((int64_t)a.T + c.L - 1) / c.L);
     } else if (a.B <= kWaveSeqs) {
-        int32_t top = 0, total = 0;   // few sequences: a walk over their starts
-        slot0 = n = 0;
-        for (int s = 0; s <= seq; ++s) {
-            top = max(top, min(max(a.cu[s], 0), a.T));
-            const int32_t y = max(top, min(max(a.cu[s + 1], 0), a.T));
-            n = (int32_t)(((int64_t)(y - top) + c.L - 1) / c.L);
-            slot0 = total;
-            total += n > 1 ? n + 1 : 0;
-        }
+        const LaneCut cut = lane_cut(a, c);
+        slot0 = __builtin_amdgcn_readlane(slot_before(cut.before - cut.ones, cut.before, threadIdx.x & 63), seq);
+        n = __builtin_amdgcn_readlane(cut.n, seq);
     } else {
         const int32_t *segments = c.maps + a.B + 1, *several = segments + a.B + 1;
         slot0 = slot_before(several[seq], segments[seq], seq);
