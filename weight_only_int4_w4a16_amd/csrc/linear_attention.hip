@@ -196,6 +196,43 @@ __device__ __forceinline__ u32x4 for_rest(Fp16, u32x4 k)
     return __builtin_bit_cast(u32x4, __builtin_bit_cast(f16x8, k) * (_Float16)(1.0f / 2048.0f));
 }
 
+// Rows of a chunk as a buffer: `n` of them, `ld` elements apart and `width` long. What lies past the last
+// row's end reads as zeros and isn't written, so that a chunk's loads need no branches: where one comes
+// between a load and its use, the compiler waits for every load in flight.
+typedef __amdgpu_buffer_rsrc_t Rows;
+__device__ __forceinline__ Rows rows_of(const void *p, int32_t n, int64_t ld, int width, int bytes)
+{
+    const uint32_t count = min(max(n, 0), kChunk);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0,
+                                             count ? ((count - 1) * (uint32_t)ld + width) * bytes : 0, 0x00027000);
+}
+template <int N>
+struct Words;
+template <>
+struct Words<1> {
+    typedef uint32_t T __attribute__((ext_vector_type(1)));
+    static __device__ __forceinline__ T load(Rows r, uint32_t at)
+    {
+        return T{__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0)};
+    }
+};
+template <>
+struct Words<2> {
+    typedef u32x2 T;
+    static __device__ __forceinline__ T load(Rows r, uint32_t at)
+    {
+        return __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+    }
+};
+// A value that is not known to stay the same: sums with it are made where they are used, instead of held in
+// registers for the whole loop.
+__device__ __forceinline__ uint32_t fresh(uint32_t x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+__device__ __forceinline__ u32x4 load4(Rows r, uint32_t at) { return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0); }
+
 template <int N>
 struct Count {
     static constexpr int value = N;
@@ -225,13 +262,32 @@ __device__ __forceinline__ uint32_t only_finite(Type t, uint32_t w)
     return w & ((o & 0x8000u ? 0u : 0xFFFFu) | (o & 0x80000000u ? 0u : 0xFFFF0000u));
 }
 
-// The power of two that brings values up to `most` below 2^15 in float16 (bfloat16 needs none).
-__device__ __forceinline__ float fit(Bf16, float) { return 1.0f; }
-__device__ __forceinline__ float fit(Fp16, float most)
+// The largest magnitude of two values and one found before. (fmaxf would first quiet each value.)
+__device__ __forceinline__ float larger(float most, float x, float y)
 {
-    if (!(most < INFINITY) || most < 0x1p-100f)
-        return 1.0f;
-    return __builtin_ldexpf(1.0f, 15 - __builtin_amdgcn_frexp_expf(most));
+    asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(most) : "v"(x), "v"(y));
+    return most;
+}
+// The largest of all lanes, of values without a sign: as integers, rotated inside rows of 16, then rows swapped.
+template <int ROTATE>
+__device__ __forceinline__ uint32_t rotated_max(uint32_t x)
+{
+    return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + ROTATE, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float wave_max(float v)
+{
+    uint32_t x = rotated_max<8>(__builtin_bit_cast(uint32_t, v));
+    x = rotated_max<1>(rotated_max<2>(rotated_max<4>(x)));
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = max(r[0], r[1]);
+    const auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return __builtin_bit_cast(float, max(s[0], s[1]));
+}
+
+// The power of two that brings values up to `most` below 2^15, for float16.
+__device__ __forceinline__ float fit(float most)
+{
+    return __builtin_ldexpf(1.0f, min(15 - __builtin_amdgcn_frexp_expf(most), 126));
 }
 
 template <int CTRL, int ROWS>
@@ -473,8 +529,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     // A lane's part of an address, in bytes; token strides are below 2^24, so it fits 32 bits.
     const uint32_t row0 = tid / pieces, dim0 = (tid % pieces) * 8;
     const uint32_t q_lane = 2 * (col * (uint32_t)a.ldq + DK / 4 * g), k_lane = 2 * (row0 * (uint32_t)a.ldk + dim0);
-    const uint32_t v_lane = 2 * (4 * g * (uint32_t)a.ldv + EV * col), o_lane = 2 * (4 * g * (uint32_t)a.ldo + EV * col);
-    const uint32_t g_lane = 4 * lane * (uint32_t)a.ldg;
+    const uint32_t v_lane = 2 * (4 * g * (uint32_t)a.ldv + EV * col + v_first), o_lane = 2 * (4 * g * (uint32_t)a.ldo + EV * col);
 
     // s[j][c][r]: row EK (4g + r) + j, column EV col + CW wave + c
     f32x4 s[EK][CW];
@@ -497,59 +552,33 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
 
     u32x4 q[contractions];   // dims (Dk / 4) g .. + Dk / 4 of token 16 it + col
     u32x4 kn[loads];
-    typedef uint32_t words __attribute__((ext_vector_type(CW)));
-    words vn[8];
+    typename Words<CW>::T vn[8];
     float gn = 0.0f;
     auto fetch_q = [&](int32_t t) {   // a chunk's rows; zeros past the segment's end
-        const int32_t n = seg.t1 - t;
-        const uint16_t *qt = qp + t * a.ldq;
-        if (n >= kChunk) {
+        const Rows rows = rows_of(qp + t * a.ldq, seg.t1 - t, a.ldq, DK, 2);
+        const uint32_t at = fresh(q_lane) + 32 * it * (uint32_t)a.ldq;
 #pragma unroll
-            for (int c = 0; c < contractions; ++c)
-                q[c] = *(const u32x4 *)((const uint8_t *)(qt + 16 * it * a.ldq + 8 * c) + q_lane);
-        } else {
-            int own = lane;   // opaque: nothing here is worth registers in the loop
-            asm volatile("" : "+v"(own));
-            const int row = 16 * it + (own & 15), at = min(row, n - 1);
-#pragma unroll
-            for (int c = 0; c < contractions; ++c)
-                q[c] = row < n ? *(const u32x4 *)(qt + at * a.ldq + DK / 4 * g + 8 * c) : u32x4{0, 0, 0, 0};
-        }
+        for (int c = 0; c < contractions; ++c)
+            q[c] = load4(rows, at + 16 * c);
     };
     // The chunk's k, v and decays in `parts` pieces, which are issued between other work: all at once
-    // they would hold up every wave at the same place. A short chunk comes with the first piece.
+    // they would hold up every wave at the same place.
     auto fetch = [&](int32_t t, auto parts_type, int part) {
         constexpr int parts = decltype(parts_type)::value;
         const int32_t n = seg.t1 - t;
-        const uint16_t *kt = kp + t * a.ldk, *vt = vp + t * a.ldv + v_first;
-        const float *gt = gp + t * a.ldg;
-        if (n >= kChunk) {
+        const uint32_t k_at = fresh(k_lane), v_at = fresh(v_lane);
+        const Rows kr = rows_of(kp + t * a.ldk, n, a.ldk, DK, 2), vr = rows_of(vp + t * a.ldv, n, a.ldv, DV, 2);
 #pragma unroll
-            for (int i = 0; i < loads; ++i)
-                if (i * parts / loads == part)
-                    kn[i] = *(const u32x4 *)((const uint8_t *)(kt + i * step * a.ldk) + k_lane);
+        for (int i = 0; i < loads; ++i)
+            if (i * parts / loads == part)
+                kn[i] = load4(kr, k_at + 2 * i * step * (uint32_t)a.ldk);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e * parts / 8 == part)
-                    vn[e] = *(const words *)(
-                        (const uint8_t *)(vt + (32 * v_half + 16 * (e / 4) + (e & 3)) * a.ldv) + v_lane);
-            if (part == parts - 1)
-                gn = *(const float *)((const uint8_t *)gt + g_lane);
-        } else if (part == 0 && n > 0) {
-            int own = lane, row_tid = tid;
-            asm volatile("" : "+v"(own), "+v"(row_tid));
-#pragma unroll
-            for (int i = 0; i < loads; ++i) {
-                const int row = row_tid / pieces + i * step, at = min(row, n - 1);
-                kn[i] = row < n ? *(const u32x4 *)(kt + at * a.ldk + dim0) : u32x4{0, 0, 0, 0};
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int row = 32 * v_half + 16 * (e / 4) + 4 * (own >> 4) + (e & 3), at = min(row, n - 1);
-                vn[e] = row < n ? *(const words *)(vt + at * a.ldv + EV * col) : words(0);
-            }
-            gn = lane < n ? gt[min(own, n - 1) * a.ldg] : 0.0f;
-        }
+        for (int e = 0; e < 8; ++e)
+            if (e * parts / 8 == part)
+                vn[e] = Words<CW>::load(vr, v_at + 2 * (32 * v_half + 16 * (e / 4) + (e & 3)) * (uint32_t)a.ldv);
+        if (part == parts - 1)
+            gn = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                               rows_of(gp + t * a.ldg, n, a.ldg, 1, 4), 4 * fresh(lane) * (uint32_t)a.ldg, 0, 0));
     };
 
     if (tid < 2) {
@@ -570,7 +599,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     }
     for (int32_t t = seg.t0; t < seg.t1; t += kChunk) {
         const int32_t n = seg.t1 - t;
-        const float gc = gn < kNone ? kNone : gn;
+        const float gc = lane >= n ? 0.0f : gn < kNone ? kNone : gn;
         const double b = running_sum((double)gc * 1.44269504088896340736);
         const uint64_t bu = __builtin_bit_cast(uint64_t, b);
         const double end = __builtin_bit_cast(
@@ -616,6 +645,8 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                     const uint32_t o = odd_bits(Type(), kn[i][e]) & 0x80008000u;
                     if (o) {
                         kn[i][e] = only_finite(Type(), kn[i][e]);
+                        if ((int)row0 + i * step >= n)   // rows that lie closer than their length: not the sequence's
+                            continue;
                         const uint32_t d = dim0 + 2 * e;   // even: both dims in one word
                         atomicMin(&lds.bad_token[parity], row0 + i * step);
                         atomicOr(&lds.bad_dims[parity][d / 32], ((o >> 15 & 1) | (o >> 30)) << (d % 32));
@@ -628,6 +659,8 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                     const uint32_t o = odd_bits(Type(), vn[e][x]), d = EV * col + v_first + 2 * x;
                     vn[e][x] = only_finite(Type(), vn[e][x]);
                     const uint32_t row = 32 * v_half + 16 * (e / 4) + 4 * g + (e & 3);
+                    if ((int)row >= n)
+                        continue;
                     if (o & 0x8000u)
                         atomicMin(&lds.bad_column[parity][d], row);
                     if (o & 0x80000000u)
@@ -649,21 +682,35 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             lds.v[v_half][v_first + 2 * x + 1][lane] = v1;
         }
         if (OUT) {
-            float most = 0.0f;
+            float shrink = 1.0f;   // bfloat16 needs none
             if constexpr (__is_same(Type, Fp16)) {
+                float most = 0.0f;
 #pragma unroll
                 for (int j = 0; j < EK; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
+                    for (int c = 0; c < CW; ++c) {
+                        most = larger(most, s[j][c][0], s[j][c][1]);
+                        most = larger(most, s[j][c][2], s[j][c][3]);
+                    }
+                most = wave_max(most);
+                if (!(most < INFINITY)) {   // the finite ones' scale
+                    rare();
+                    most = 0.0f;
 #pragma unroll
-                        for (int c = 0; c < CW; ++c)
-                            most = fmaxf(most, fabsf(s[j][c][r]));
-                for (int d = 1; d < 64; d <<= 1)
-                    most = fmaxf(most, __shfl_xor(most, d));
+                    for (int j = 0; j < EK; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int c = 0; c < CW; ++c) {
+                                const float x = fabsf(s[j][c][r]);
+                                most = x < INFINITY && x > most ? x : most;
+                            }
+                    most = wave_max(most);
+                }
+                shrink = fit(most);
+                if (lane == 0)
+                    lds.grow[wave] = 1.0f / shrink;
             }
-            const float shrink = fit(Type(), most);
-            if (__is_same(Type, Fp16) && lane == 0)
-                lds.grow[wave] = 1.0f / shrink;
 #pragma unroll
             for (int p = 0; p < WK; ++p)
 #pragma unroll
@@ -680,12 +727,17 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                 lds.b[lane] = (float)b;
                 lds.eb[lane] = a.scale * __builtin_amdgcn_exp2f((float)b);
             }
-            lds.ed[lane] = __builtin_amdgcn_exp2f((float)(end - b));
+            lds.ed[lane] = lane < n ? __builtin_amdgcn_exp2f((float)(end - b)) : 0.0f;
         }
         __syncthreads();
         odd = __builtin_amdgcn_readfirstlane(lds.odd[parity]) != 0;
         __builtin_amdgcn_sched_barrier(0);
 
+        if (OUT) {   // on both ways: queries still on their way on one of them would be waited for behind it
+#pragma unroll
+            for (int c = 0; c < contractions; ++c)
+                asm volatile("" : "+v"(q[c]));
+        }
         if (OUT && it * 16 < n) {
             f32x4 o[EV];
 #pragma unroll
@@ -746,25 +798,25 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                         o[j][r] = 16 * it + 4 * g + r >= bad ? NAN : o[j][r];
                 }
             }
-            uint16_t *ot = op + (t + 16 * it) * a.ldo;
+            const Rows rows = rows_of(op + t * a.ldo, n, a.ldo, DV, 2);
+            const uint32_t o_at = fresh(o_lane);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (16 * it + 4 * g + r < n) {
-                    uint32_t x[EV / 2];
+            for (int r = 0; r < 4; ++r) {
+                uint32_t x[EV / 2];
 #pragma unroll
-                    for (int j = 0; j < EV; j += 2)
-                        x[j / 2] = pack2(Type(), o[j][r], o[j + 1][r]);
-                    uint8_t *to = (uint8_t *)(ot + r * a.ldo) + o_lane;
-                    if constexpr (EV == 8)
-                        *(u32x4 *)to = u32x4{x[0], x[1], x[2], x[3]};
-                    else
-                        *(u32x2 *)to = u32x2{x[0], x[1]};
-                }
+                for (int j = 0; j < EV; j += 2)
+                    x[j / 2] = pack2(Type(), o[j][r], o[j + 1][r]);
+                const uint32_t at = 16 * it + 4 * g + r < n ? o_at + 2 * (16 * it + r) * (uint32_t)a.ldo : ~0u;
+                if constexpr (EV == 8)
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{x[0], x[1], x[2], x[3]}, rows, at, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b64(u32x2{x[0], x[1]}, rows, at, 0, 0);
+            }
         }
 
         if (OUT && n <= kChunk && !REST)
             break;   // nobody reads the state after this segment
-        if (OUT && n > kChunk)
+        if (OUT)
             fetch_q(t + kChunk);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
