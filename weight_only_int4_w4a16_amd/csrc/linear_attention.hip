@@ -565,7 +565,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     // they would hold up every wave at the same place.
     auto fetch = [&](int32_t t, auto parts_type, int part) {
         constexpr int parts = decltype(parts_type)::value;
-        const int32_t n = seg.t1 - t;
+        const int32_t n = t < seg.t0 ? 0 : seg.t1 - t;
         const uint32_t k_at = fresh(k_lane), v_at = fresh(v_lane);
         const Rows kr = rows_of(kp + t * a.ldk, n, a.ldk, DK, 2), vr = rows_of(vp + t * a.ldv, n, a.ldv, DV, 2);
 #pragma unroll
@@ -591,13 +591,18 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
         lds.bad_column[i & 1][i >> 1] = kChunk;
     bool odd = false;
 
-    double whole = 0.0;   // sum of log2 decays of the segment
-    if (seg.t0 < seg.t1) {
-        fetch(seg.t0, Count<1>(), 0);
+    // What a segment adds is summed from its last chunk to its first: a chunk then weighs as much as the
+    // decays behind it say, and the sum needs no factor per chunk (a tenth of the work outside the products).
+    double whole = 0.0;   // sum of log2 decays of the segment's chunks so far
+    constexpr int32_t way = OUT ? kChunk : -kChunk;
+    const int32_t chunks = (seg.t1 - seg.t0 + kChunk - 1) / kChunk;
+    int32_t t = OUT ? seg.t0 : seg.t0 + (chunks - 1) * kChunk;
+    if (chunks > 0) {
+        fetch(t, Count<1>(), 0);
         if (OUT)
-            fetch_q(seg.t0);
+            fetch_q(t);
     }
-    for (int32_t t = seg.t0; t < seg.t1; t += kChunk) {
+    for (int32_t left_over = chunks; left_over > 0; --left_over, t += way) {
         const int32_t n = seg.t1 - t;
         const float gc = lane >= n ? 0.0f : gn < kNone ? kNone : gn;
         const double b = running_sum((double)gc * 1.44269504088896340736);
@@ -606,8 +611,9 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(bu >> 32), 63) << 32 |
                         (uint32_t)__builtin_amdgcn_readlane((int)bu, 63));
         const float whole_chunk = __builtin_amdgcn_exp2f((float)end);
+        const double behind = OUT ? end : whole + end;
         whole += end;
-        const int parity = ((t - seg.t0) / kChunk) & 1;
+        const int parity = left_over & 1;
         __syncthreads();   // the previous chunk has been read
 
         // Values of k and v that are not finite (rare) become zeros and mark what they reach: the
@@ -727,7 +733,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                 lds.b[lane] = (float)b;
                 lds.eb[lane] = a.scale * __builtin_amdgcn_exp2f((float)b);
             }
-            lds.ed[lane] = lane < n ? __builtin_amdgcn_exp2f((float)(end - b)) : 0.0f;
+            lds.ed[lane] = lane < n ? __builtin_amdgcn_exp2f((float)(behind - b)) : 0.0f;
         }
         __syncthreads();
         odd = __builtin_amdgcn_readfirstlane(lds.odd[parity]) != 0;
@@ -825,7 +831,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             for (int r = 0; r < 4; ++r) {
 #pragma unroll
                 for (int c = 0; c < CW; ++c)
-                    s[j][c][r] *= whole_chunk;
+                    s[j][c][r] = OUT ? s[j][c][r] * whole_chunk : s[j][c][r];
             }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -860,7 +866,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
 #pragma unroll
             for (int w = 0; w < WK; ++w) {
                 if (!OUT) {
-                    fetch(t + kChunk, Count<2 * WK>(), half * WK + w);
+                    fetch(t + way, Count<2 * WK>(), half * WK + w);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 u32x4 k0, k1;   // dims EK col + 2w and + 2w + 1
