@@ -200,7 +200,7 @@ __device__ __forceinline__ u32x4 for_rest(Fp16, u32x4 k)
 // row's end reads as zeros and isn't written, so that a chunk's loads need no branches: where one comes
 // between a load and its use, the compiler waits for every load in flight.
 typedef __amdgpu_buffer_rsrc_t Rows;
-__device__ __forceinline__ Rows rows_of(const void *p, int32_t n, int64_t ld, int width, int bytes)
+__device__ __forceinline__ Rows rows_of(const void *p, int32_t n, int32_t ld, int width, int bytes)
 {
     const uint32_t count = min(max(n, 0), kChunk);
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0,
@@ -229,6 +229,11 @@ struct Words<2> {
 __device__ __forceinline__ uint32_t fresh(uint32_t x)
 {
     asm volatile("" : "+v"(x));
+    return x;
+}
+__device__ __forceinline__ int32_t fresh_scalar(int32_t x)
+{
+    asm volatile("" : "+s"(x));
     return x;
 }
 __device__ __forceinline__ u32x4 load4(Rows r, uint32_t at) { return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0); }
@@ -512,6 +517,8 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     constexpr int threads = kSegmentThreads, NW = threads / 64, EK = DK / 16, WK = EK / 2, EV = DV / 16, CW = EV / NW;
     constexpr int pieces = DK / 8, loads = kChunk * pieces / threads, step = threads / pieces;
     constexpr int contractions = DK / 32;
+    const int32_t ldq = (int32_t)a.ldq, ldk = (int32_t)a.ldk, ldv = (int32_t)a.ldv, ldo = (int32_t)a.ldo;   // below 2^24
+    const int32_t ldg = (int32_t)a.ldg;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4, h = blockIdx.x;
     const int hk = h / (a.H / a.Hk);
@@ -528,8 +535,8 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     const int v_half = 2 * CW * wave / EV, v_first = 2 * CW * wave % EV;
     // A lane's part of an address, in bytes; token strides are below 2^24, so it fits 32 bits.
     const uint32_t row0 = tid / pieces, dim0 = (tid % pieces) * 8;
-    const uint32_t q_lane = 2 * (col * (uint32_t)a.ldq + DK / 4 * g), k_lane = 2 * (row0 * (uint32_t)a.ldk + dim0);
-    const uint32_t v_lane = 2 * (4 * g * (uint32_t)a.ldv + EV * col + v_first), o_lane = 2 * (4 * g * (uint32_t)a.ldo + EV * col);
+    const uint32_t q_lane = 2 * (col * (uint32_t)ldq + DK / 4 * g), k_lane = 2 * (row0 * (uint32_t)ldk + dim0);
+    const uint32_t v_lane = 2 * (4 * g * (uint32_t)ldv + EV * col + v_first), o_lane = 2 * (4 * g * (uint32_t)ldo + EV * col);
 
     // s[j][c][r]: row EK (4g + r) + j, column EV col + CW wave + c
     f32x4 s[EK][CW];
@@ -555,8 +562,9 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     typename Words<CW>::T vn[8];
     float gn = 0.0f;
     auto fetch_q = [&](int32_t t) {   // a chunk's rows; zeros past the segment's end
-        const Rows rows = rows_of(qp + t * a.ldq, seg.t1 - t, a.ldq, DK, 2);
-        const uint32_t at = fresh(q_lane) + 32 * it * (uint32_t)a.ldq;
+        const int32_t ldq = fresh_scalar((int32_t)a.ldq);
+        const Rows rows = rows_of(qp + (int64_t)t * ldq, seg.t1 - t, ldq, DK, 2);
+        const uint32_t at = fresh(q_lane) + 32 * it * (uint32_t)ldq;
 #pragma unroll
         for (int c = 0; c < contractions; ++c)
             q[c] = load4(rows, at + 16 * c);
@@ -566,19 +574,20 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     auto fetch = [&](int32_t t, auto parts_type, int part) {
         constexpr int parts = decltype(parts_type)::value;
         const int32_t n = t < seg.t0 ? 0 : seg.t1 - t;
+        const int32_t ldk = fresh_scalar((int32_t)a.ldk), ldv = fresh_scalar((int32_t)a.ldv), ldg = fresh_scalar((int32_t)a.ldg);
         const uint32_t k_at = fresh(k_lane), v_at = fresh(v_lane);
-        const Rows kr = rows_of(kp + t * a.ldk, n, a.ldk, DK, 2), vr = rows_of(vp + t * a.ldv, n, a.ldv, DV, 2);
+        const Rows kr = rows_of(kp + (int64_t)t * ldk, n, ldk, DK, 2), vr = rows_of(vp + (int64_t)t * ldv, n, ldv, DV, 2);
 #pragma unroll
         for (int i = 0; i < loads; ++i)
             if (i * parts / loads == part)
-                kn[i] = load4(kr, k_at + 2 * i * step * (uint32_t)a.ldk);
+                kn[i] = load4(kr, k_at + 2 * i * step * (uint32_t)ldk);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (e * parts / 8 == part)
-                vn[e] = Words<CW>::load(vr, v_at + 2 * (32 * v_half + 16 * (e / 4) + (e & 3)) * (uint32_t)a.ldv);
+                vn[e] = Words<CW>::load(vr, v_at + 2 * (32 * v_half + 16 * (e / 4) + (e & 3)) * (uint32_t)ldv);
         if (part == parts - 1)
             gn = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                               rows_of(gp + t * a.ldg, n, a.ldg, 1, 4), 4 * fresh(lane) * (uint32_t)a.ldg, 0, 0));
+                                               rows_of(gp + (int64_t)t * ldg, n, ldg, 1, 4), 4 * fresh(lane) * (uint32_t)ldg, 0, 0));
     };
 
     if (tid < 2) {
@@ -804,7 +813,8 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                         o[j][r] = 16 * it + 4 * g + r >= bad ? NAN : o[j][r];
                 }
             }
-            const Rows rows = rows_of(op + t * a.ldo, n, a.ldo, DV, 2);
+            const int32_t ldo = fresh_scalar((int32_t)a.ldo);
+            const Rows rows = rows_of(op + (int64_t)t * ldo, n, ldo, DV, 2);
             const uint32_t o_at = fresh(o_lane);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -812,7 +822,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
 #pragma unroll
                 for (int j = 0; j < EV; j += 2)
                     x[j / 2] = pack2(Type(), o[j][r], o[j + 1][r]);
-                const uint32_t at = 16 * it + 4 * g + r < n ? o_at + 2 * (16 * it + r) * (uint32_t)a.ldo : ~0u;
+                const uint32_t at = 16 * it + 4 * g + r < n ? o_at + 2 * (16 * it + r) * (uint32_t)ldo : ~0u;
                 if constexpr (EV == 8)
                     __builtin_amdgcn_raw_buffer_store_b128(u32x4{x[0], x[1], x[2], x[3]}, rows, at, 0, 0);
                 else
