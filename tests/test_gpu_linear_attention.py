@@ -339,3 +339,46 @@ def test_step_resets_and_empty():
     assert float((s[1].cpu().double() - want).abs().max()) <= 2.0 ** -23 * float(want.abs().max())
     none = w.linear_attention_step(q[:0], k[:0], v[:0], g[:0], s[:0])
     assert none.shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("n", [1, 70, 130])
+def test_rows_that_share_memory(n):
+    x = Linear([n], 4, 2, 128, 64, seed=n + 900)
+    x.q, x.k, x.v = (t[:1].expand(n, -1, -1) for t in (x.q, x.k, x.v))
+    kw = {name: getattr(x, name)[:1].cuda().expand(n, -1, -1) for name in "qkv"}
+    assert n == 1 or kw["k"].stride(0) == 0
+    x.check(*x.run(**kw))
+
+
+@pytest.mark.parametrize("stride", [0, 8, 64])
+def test_one_token_of_any_stride(stride):
+    x = Linear([1], 3, 3, 64, 128, dtype=torch.float16, seed=stride + 950)
+    kw = {name: getattr(x, name).cuda() for name in "qkv"}
+    kw = {name: t.as_strided(t.shape, (stride,) + t.stride()[1:]) for name, t in kw.items()}
+    buf = torch.full((4, 3, 128), 7.0, dtype=torch.float16, device="cuda")
+    out = buf[:1].as_strided((1, 3, 128), (stride, 128, 1))
+    o, state = x.run(out=out, **kw)
+    x.check(o, state)
+    assert bool((buf[1:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_infinite_state_entry_beside_large_ones(dtype):
+    x = Linear([100], 2, 2, 128, 128, dtype=dtype, seed=77)
+    x.state *= 3e5   # past float16's range
+    state = x.state.clone()
+    state[0, :, 3, 5] = math.inf
+    out, end = x.run(state=state.cuda())
+    assert not bool(torch.isfinite(out[:, :, 5]).any())
+    assert not bool(torch.isfinite(end[0, :, 3, 5]).any())
+    out[:, :, 5] = 0
+    x.v[:, :, 5] = 0   # the column apart, all as without it
+    x.state[0, :, :, 5] = 0
+    end[0, :, :, 5] = 0
+    # what rounds past the type's largest value is an infinity of its sign
+    want = mo.linear(x.q.double(), x.k.double(), x.v.double(), x.g.double(), x.state[0].double(), x.scale)[0]
+    top = torch.finfo(dtype).max
+    out = out.cpu().double()
+    over = out.isinf() & (want.abs() * (1 + 2 * mo.half_step(dtype)) > top) & (out.sign() == want.sign())
+    assert not bool((~over & (want.abs() * (1 - 2 * mo.half_step(dtype)) > top)).any())
+    x.check(torch.where(over, want, out), end)
