@@ -845,7 +845,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            constexpr int terms = REST ? Terms<Type>::count : 1;
+            constexpr int terms = REST ? Terms<Type>::count : Terms<Type>::count - 1;
             u32x4 x[terms][CW];   // e^(b_63 - b_j) v_j, rounded, and what the rounding leaves
 #pragma unroll
             for (int c = 0; c < CW; ++c)
