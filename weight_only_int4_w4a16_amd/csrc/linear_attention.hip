@@ -114,8 +114,10 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 // the log decays inside a chunk (its own token included) and S the state before it, per head:
 //   o_i = scale * (e^{b_i} q_i^T S + sum_{j<=i} e^{b_i - b_j} (q_i . k_j) v_j)
 //   S  <- e^{b_63} S + sum_j k_j (e^{b_63 - b_j} v_j)^T
-// All products are MFMA 16x16x32. A wave owns 32 of the Dv columns, with its part of S in registers in
-// float32, so waves share nothing but the chunk's q and k in LDS; every wave forms all the scores.
+// All products are MFMA 16x16x32. Of the state a wave owns a quarter of the Dv columns, in registers in
+// float32; of the outputs a tile of 16 tokens, so scores are formed once. k, the state rounded for q S and
+// the rows of v in operand order are shared through LDS, two barriers per chunk; the next chunk's rows
+// are on their way during the products.
 //
 // Operands never cross lanes. A contraction's order is free as long as both operands agree:
 //   scores are formed transposed (k q^T): a lane then holds token i = lane % 16 of a tile of queries and
@@ -125,15 +127,25 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 //   consecutive values of k rows give them; two tiles are the second operand of the product q S, whose
 //   first operand, q at dk = EK (4g + r) + {j, j + 1}, are words that the lane has loaded for the scores.
 //
-// Roundings: scores with their decay, S in q S, and e^{b_63 - b_j} v_j are rounded to the type for
-// their products, the last one kept as a sum of three bfloat16 or two float16 values (24 and 22 bits) where
-// the result reaches a returned state. Decays are summed in float64 over a chunk; the scores' take the sums in float32, off by 2^-24
-// of their size. A log decay below -104 counts as that: e^-104 is zero in float32, and so a state that
-// is cleared by -inf costs its neighbours few digits.
+// Roundings, all to the type for a matrix product (float32 products would take eight times the matrix
+// units' time): scores with their decay; S in q S, where the outputs' own rounding is as large; and
+// e^{b_63 - b_j} v_j, kept as a sum of three bfloat16 or two float16 values (24 and 22 bits) where the
+// result reaches a returned state or another segment, else of two bfloat16 or one float16. With that
+// outputs of 32768 bfloat16 tokens are off by 2.35e-3 of their norm (2.57e-3 with one bfloat16 value,
+// 1.66e-3 by their own rounding alone; S in float16 as well would make it 2.0e-3 for another 20 us of 400),
+// states by 5e-7. Decays are summed in float64 over a chunk; the scores' take the sums in float32, off by
+// 2^-24 of their size. A log decay below -104 counts as that: e^-104 is zero in float32, and so a state
+// that is cleared by -inf costs its neighbours few digits.
 //
-// One segment per sequence needs one launch. Longer ones take three: what each segment but the last
-// adds to a state (K and V read once), the states before every segment (a running sum over
-// segments), then the outputs of all segments side by side.
+// One segment per sequence needs one launch. Longer ones take three: what each segment adds to a state
+// (k and v read once), the states before every segment and after the last (a running sum over segments),
+// then the outputs of all segments side by side.
+//
+// What bounds it (128 x 128, 32 heads of 32768 bfloat16 tokens, 398 us in all): the outputs move 1.07 GB in
+// 240 to 255 us (4.2 to 4.5 TB/s, where a copy of 4 GiB reaches 4.7); the segments' sums read 0.54 GB in 173 us, with
+// the vector units busy for 47 and the matrix units for 29 % of it (the three terms). A short sequence
+// is bound by the chain of its chunks, 4.5 us each: two barriers, and between them the products of a
+// wave, which are alone on their SIMD.
 constexpr int kChunk = 64;
 constexpr int kSegmentThreads = 256;
 constexpr float kNone = -104.0f;
@@ -1023,14 +1035,20 @@ hipError_t linear_typed(const LinearArgs &a, const Cuts &c, hipStream_t stream)
     return a.Dv == 64 ? linear_of<Type, 128, 64>(a, c, stream) : linear_of<Type, 128, 128>(a, c, stream);
 }
 
-// Tokens per segment: enough segments for two work-groups per CU of a 256-CU device, but not so short
-// that reading and writing their states (256 KB per segment and head of 128 x 128, against 1.5 KB per
-// token) weighs, and no more segments than the grid takes.
+// Tokens per segment, as many as leave one segment per CU of a 256-CU device and at least 128; past 512
+// tokens as many as leave two. A segment's state is written and read once (128 KB per head of 128 x 128,
+// against 1.5 KB per token), so longer ones move less and shorter ones end sooner. Measured, us for
+// tokens x heads of 128 x 128, bfloat16, with segments of 128 / 256 / 512: 700 x 8 26 / 38 / 64,
+// 2048 x 8 31 / 41 / 66, 1024 x 32 41 / 44 / 68, 2048 x 32 66 / 54 / 70, 8192 x 8 84 / 65 / 75; of 512
+// and 1024: 8192 x 32 118 and 134; of 1024, 2048 and 4096: 32768 x 32 446, 400 and 469. Up to 256 tokens
+// in all, where a cut can only halve them, it costs more than it gives (200 x 16: 24 and 22).
 int32_t segment_length(int32_t T, int32_t H)
 {
-    int64_t L = ((int64_t)T * H / 512 + kChunk - 1) / kChunk * kChunk;
-    if (L < 512)
-        L = 512;
+    const int64_t all = (int64_t)T * H;
+    int64_t L = all / 256 < 512 ? all / 256 : all / 512 < 512 ? 512 : all / 512;
+    L = (L + kChunk - 1) / kChunk * kChunk;
+    if (L < (T <= 256 ? 256 : 128))
+        L = T <= 256 ? 256 : 128;
     if (L > 4096)
         L = 4096;
     while (T / L > 16384)
