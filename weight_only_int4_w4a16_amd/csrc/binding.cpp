@@ -1,8 +1,8 @@
 // The short way from Python into the token mixers' C entries: checks and marshals the arguments of a
-// call whose tensors are all given, in C++, without ctypes (a single-token state update 10.5 -> 3.7 us a call, a
-// cache write of 16 tokens 9.8 -> 3.7 us). Every
-// function returns the entry's status, or -1 where an argument is not what it takes; the caller then
-// goes the long way (mixers.py), which allocates, switches devices, or raises.
+// call whose tensors are all given, in C++, without ctypes (a single-token state update 10.5 -> 3.7 us
+// a call, a cache write of 16 tokens 9.8 -> 3.7 us). Every function returns the entry's status, or -1
+// where an argument is not what it takes; the caller then goes the long way (mixers.py), which
+// allocates, switches devices, or raises.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
