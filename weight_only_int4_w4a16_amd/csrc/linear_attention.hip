@@ -248,7 +248,10 @@ __device__ __forceinline__ int32_t fresh_scalar(int32_t x)
     asm volatile("" : "+s"(x));
     return x;
 }
-__device__ __forceinline__ u32x4 load4(Rows r, uint32_t at) { return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0); }
+__device__ __forceinline__ u32x4 load4(Rows r, uint32_t at)
+{
+    return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+}
 
 template <int N>
 struct Count {
@@ -512,7 +515,7 @@ struct ChunkLds {
     u32x4 v[2][DV / 16][64];                          // second operands: half of the chunk, column
     u32x4 s[OUT ? DK / 32 : 1][OUT ? DV / 16 : 1][64];   // and the state's: pair of tiles, column
     float b[kChunk], eb[kChunk], ed[kChunk];          // per token: b (log2), scale e^b, e^(b_63 - b)
-    float grow[kSegmentThreads / 64];                              // a wave's part of s is smaller by this
+    float grow[kSegmentThreads / 64];                 // a wave's part of s is smaller by this
     // What is not finite, in even and odd chunks: whether, first token of k, dims of k, first tokens of v
     uint32_t odd[2], bad_token[2], bad_dims[2][DK / 32], bad_column[2][DV];
 };
@@ -529,8 +532,8 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     constexpr int threads = kSegmentThreads, NW = threads / 64, EK = DK / 16, WK = EK / 2, EV = DV / 16, CW = EV / NW;
     constexpr int pieces = DK / 8, loads = kChunk * pieces / threads, step = threads / pieces;
     constexpr int contractions = DK / 32;
-    const int32_t ldq = (int32_t)a.ldq, ldk = (int32_t)a.ldk, ldv = (int32_t)a.ldv, ldo = (int32_t)a.ldo;   // below 2^24
-    const int32_t ldg = (int32_t)a.ldg;
+    // below 2^24
+    const int32_t ldq = (int32_t)a.ldq, ldk = (int32_t)a.ldk, ldv = (int32_t)a.ldv, ldo = (int32_t)a.ldo;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4, h = blockIdx.x;
     const int hk = h / (a.H / a.Hk);
@@ -548,7 +551,8 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     // A lane's part of an address, in bytes; token strides are below 2^24, so it fits 32 bits.
     const uint32_t row0 = tid / pieces, dim0 = (tid % pieces) * 8;
     const uint32_t q_lane = 2 * (col * (uint32_t)ldq + DK / 4 * g), k_lane = 2 * (row0 * (uint32_t)ldk + dim0);
-    const uint32_t v_lane = 2 * (4 * g * (uint32_t)ldv + EV * col + v_first), o_lane = 2 * (4 * g * (uint32_t)ldo + EV * col);
+    const uint32_t v_lane = 2 * (4 * g * (uint32_t)ldv + EV * col + v_first);
+    const uint32_t o_lane = 2 * (4 * g * (uint32_t)ldo + EV * col);
 
     // s[j][c][r]: row EK (4g + r) + j, column EV col + CW wave + c
     f32x4 s[EK][CW];
@@ -586,9 +590,11 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
     auto fetch = [&](int32_t t, auto parts_type, int part) {
         constexpr int parts = decltype(parts_type)::value;
         const int32_t n = t < seg.t0 ? 0 : seg.t1 - t;
-        const int32_t ldk = fresh_scalar((int32_t)a.ldk), ldv = fresh_scalar((int32_t)a.ldv), ldg = fresh_scalar((int32_t)a.ldg);
+        const int32_t ldk = fresh_scalar((int32_t)a.ldk), ldv = fresh_scalar((int32_t)a.ldv);
+        const int32_t ldg = fresh_scalar((int32_t)a.ldg);
         const uint32_t k_at = fresh(k_lane), v_at = fresh(v_lane);
-        const Rows kr = rows_of(kp + (int64_t)t * ldk, n, ldk, DK, 2), vr = rows_of(vp + (int64_t)t * ldv, n, ldv, DV, 2);
+        const Rows kr = rows_of(kp + (int64_t)t * ldk, n, ldk, DK, 2);
+        const Rows vr = rows_of(vp + (int64_t)t * ldv, n, ldv, DV, 2);
 #pragma unroll
         for (int i = 0; i < loads; ++i)
             if (i * parts / loads == part)
@@ -598,8 +604,8 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             if (e * parts / 8 == part)
                 vn[e] = Words<CW>::load(vr, v_at + 2 * (32 * v_half + 16 * (e / 4) + (e & 3)) * (uint32_t)ldv);
         if (part == parts - 1)
-            gn = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                               rows_of(gp + (int64_t)t * ldg, n, ldg, 1, 4), 4 * fresh(lane) * (uint32_t)ldg, 0, 0));
+            gn = __builtin_bit_cast(float, Words<1>::load(rows_of(gp + (int64_t)t * ldg, n, ldg, 1, 4),
+                                                          4 * fresh(lane) * (uint32_t)ldg)[0]);
     };
 
     if (tid < 2) {
@@ -623,7 +629,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
         if (OUT)
             fetch_q(t);
     }
-    for (int32_t left_over = chunks; left_over > 0; --left_over, t += way) {
+    for (int32_t chunks_left = chunks; chunks_left > 0; --chunks_left, t += way) {
         const int32_t n = seg.t1 - t;
         const float gc = lane >= n ? 0.0f : gn < kNone ? kNone : gn;
         const double b = running_sum((double)gc * 1.44269504088896340736);
@@ -634,7 +640,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
         const float whole_chunk = __builtin_amdgcn_exp2f((float)end);
         const double behind = OUT ? end : whole + end;
         whole += end;
-        const int parity = left_over & 1;
+        const int parity = chunks_left & 1;
         __syncthreads();   // the previous chunk has been read
 
         // Values of k and v that are not finite (rare) become zeros and mark what they reach: the
