@@ -382,3 +382,20 @@ def test_infinite_state_entry_beside_large_ones(dtype):
     over = out.isinf() & (want.abs() * (1 + 2 * mo.half_step(dtype)) > top) & (out.sign() == want.sign())
     assert not bool((~over & (want.abs() * (1 - 2 * mo.half_step(dtype)) > top)).any())
     x.check(torch.where(over, want, out), end)
+
+
+def test_offsets_past_32_bits():
+    n, ld = 130, 2 ** 24 - 8   # the longest strides: a chunk's rows lie up to 2^31 bytes apart
+    x = Linear([n], 2, 1, 128, 64, seed=990)
+
+    def far(t, dtype):
+        big = torch.empty((n - 1) * ld + t[0].numel(), dtype=dtype, device="cuda")
+        return big.as_strided(t.shape, (ld,) + t.stride()[1:])
+
+    kw = {}
+    for name in "qkvg":
+        t = getattr(x, name)
+        kw[name] = far(t, t.dtype)
+        kw[name].copy_(t)
+    out = far(x.v, x.dtype)
+    x.check(*x.run(out=out, **kw))
