@@ -137,6 +137,11 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 // 2^-24 of their size. A log decay below -104 counts as that: e^-104 is zero in float32, and so a state
 // that is cleared by -inf costs its neighbours few digits.
 //
+// Scores have more range than float16. Those of a query are bounded by its norm, the chunk's largest norm of a
+// key (from sums of squares, which also show what is not finite) and the largest e^{b_i - b_j} where decays are
+// positive; the power of two that brings this bound to 2^15 goes with e^{b_i} and is taken back from the
+// query's sum. Scores below 2^-29 of the bound lose digits. (Costs 0.3 us of 43 for nine sequences of up to 300 tokens.)
+//
 // One segment per sequence needs one launch. Longer ones take three: what each segment adds to a state
 // (k and v read once), the states before every segment and after the last (a running sum over segments),
 // then the outputs of all segments side by side.
@@ -206,6 +211,27 @@ __device__ __forceinline__ u32x4 for_rest(Bf16, u32x4 k) { return k; }
 __device__ __forceinline__ u32x4 for_rest(Fp16, u32x4 k)
 {
     return __builtin_bit_cast(u32x4, __builtin_bit_cast(f16x8, k) * (_Float16)(1.0f / 2048.0f));
+}
+// Sum over the four lanes that share lane % 16.
+__device__ __forceinline__ float sum4(float v)
+{
+    uint32_t x = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    v = __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+    x = __builtin_bit_cast(uint32_t, v);
+    const auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return __builtin_bit_cast(float, (uint32_t)s[0]) + __builtin_bit_cast(float, (uint32_t)s[1]);
+}
+// acc plus the squares of a pair. (Should subnormal values count as zeros there, root_exponent covers it.)
+__device__ __forceinline__ float add_squares(uint32_t w, float acc)
+{
+    const f16x2 x = __builtin_bit_cast(f16x2, w);
+    return __builtin_amdgcn_fdot2(x, x, acc, false);
+}
+// e with sqrt(sum) <= 2^e, where up to 2^7 float16 subnormals may be missing in the sum.
+__device__ __forceinline__ int32_t root_exponent(float sum)
+{
+    return (__builtin_amdgcn_frexp_expf(fmaxf(sum, 0x1p-21f)) + 1) >> 1;
 }
 
 // Rows of a chunk as a buffer: `n` of them, `ld` elements apart and `width` long. What lies past the last
@@ -509,13 +535,17 @@ __global__ __launch_bounds__(kMapThreads) void linear_maps_kernel(LinearArgs a, 
     }
 }
 
-template <int DK, int DV, bool OUT>
+template <class Type, int DK, int DV, bool OUT>
 struct ChunkLds {
+    static constexpr bool fp16 = __is_same(Type, Fp16);
     uint16_t k[kChunk][DK + 8];
     u32x4 v[2][DV / 16][64];                          // second operands: half of the chunk, column
     u32x4 s[OUT ? DK / 32 : 1][OUT ? DV / 16 : 1][64];   // and the state's: pair of tiles, column
-    float b[kChunk], eb[kChunk], ed[kChunk];          // per token: b (log2), scale e^b, e^(b_63 - b)
+    float b[kChunk], eb[kChunk], ed[kChunk];          // per token: b (log2), scale e^b (bfloat16), e^(b_63 - b)
     float grow[kSegmentThreads / 64];                 // a wave's part of s is smaller by this
+    // float16: sums of squares of k; a wave's queries' factors, before and after the products with v
+    float squares[kSegmentThreads / 64];
+    float row[fp16 && OUT ? kSegmentThreads / 64 : 1][16], last[fp16 && OUT ? kSegmentThreads / 64 : 1][16];
     // What is not finite, in even and odd chunks: whether, first token of k, dims of k, first tokens of v
     uint32_t odd[2], bad_token[2], bad_dims[2][DK / 32], bad_column[2][DV];
 };
@@ -526,8 +556,9 @@ struct ChunkLds {
 // several as well, those few work-groups alone took 340 us where the others took 230.)
 template <class Type, int DK, int DV, bool OUT, bool REST>
 __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cuts, const Segment &seg,
-                                            ChunkLds<DK, DV, OUT> &lds)
+                                            ChunkLds<Type, DK, DV, OUT> &lds)
 {
+    constexpr bool fp16 = __is_same(Type, Fp16);
     // a wave owns CW of the EV columns of a lane
     constexpr int threads = kSegmentThreads, NW = threads / 64, EK = DK / 16, WK = EK / 2, EV = DV / 16, CW = EV / NW;
     constexpr int pieces = DK / 8, loads = kChunk * pieces / threads, step = threads / pieces;
@@ -640,6 +671,19 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
         const float whole_chunk = __builtin_amdgcn_exp2f((float)end);
         const double behind = OUT ? end : whole + end;
         whole += end;
+        float gain = 0.0f;   // float16: the largest b_i - b_j of a token, which is 0 without growth
+        if constexpr (fp16 && OUT) {
+            if (__ballot(gc > 0.0f)) {
+                rare();
+                float x = (float)b;
+                for (int d = 1; d < 64; d <<= 1) {
+                    const float o = __shfl_up(x, d);
+                    if (lane >= d)
+                        x = fminf(x, o);
+                }
+                gain = __shfl((float)b - x, 16 * it + col);
+            }
+        }
         const int parity = chunks_left & 1;
         __syncthreads();   // the previous chunk has been read
 
@@ -657,12 +701,26 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             for (int i = tid; i < DV; i += threads)
                 lds.bad_column[parity ^ 1][i] = kChunk;
         }
+        float squares = 0.0f;
+        auto add_up = [&]() {
+            squares = 0.0f;
+#pragma unroll
+            for (int i = 0; i < loads; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    squares = add_squares(kn[i][e], squares);
+        };
         float seen = 0.0f;   // 0, or NaN where something is not finite
+        if constexpr (fp16) {
+            add_up();
+            seen = squares * 0.0f;
+        } else {
 #pragma unroll
-        for (int i = 0; i < loads; ++i)
+            for (int i = 0; i < loads; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                seen = times_zero(Type(), kn[i][e], seen);
+                for (int e = 0; e < 4; ++e)
+                    seen = times_zero(Type(), kn[i][e], seen);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
 #pragma unroll
@@ -699,6 +757,13 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                     if (o & 0x80000000u)
                         atomicMin(&lds.bad_column[parity][d + 1], row);
                 }
+            if constexpr (fp16)
+                add_up();
+        }
+        if constexpr (fp16) {
+            squares = wave_max(squares);
+            if (lane == 0)
+                lds.squares[wave] = squares;
         }
 #pragma unroll
         for (int i = 0; i < loads; ++i)
@@ -758,7 +823,8 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
         if (wave == 0) {
             if (OUT) {
                 lds.b[lane] = (float)b;
-                lds.eb[lane] = a.scale * __builtin_amdgcn_exp2f((float)b);
+                if constexpr (!fp16)
+                    lds.eb[lane] = a.scale * __builtin_amdgcn_exp2f((float)b);
             }
             lds.ed[lane] = lane < n ? __builtin_amdgcn_exp2f((float)(behind - b)) : 0.0f;
         }
@@ -788,15 +854,36 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                 for (int j = 0; j < EV; ++j)
                     o[j] = mfma(Type(), x, lds.s[p][j][lane], o[j]);
             }
-            const f32x4 row = *(const f32x4 *)&lds.eb[16 * it + 4 * g];
+            float bi = lds.b[16 * it + col];
+            f32x4 row;   // factors of tokens 16 it + 4g ..
+            if constexpr (fp16) {   // no score of token 16 it + col is above 2^-e, from the norms of q and k
+                float norm = 0.0f;
+#pragma unroll
+                for (int c = 0; c < contractions; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        norm = add_squares(q[c][e], norm);
+                const f32x4 k2 = *(const f32x4 *)lds.squares;   // a row's squares are those of `pieces` lanes
+                const float k_norm = fmaxf(fmaxf(k2[0], k2[1]), fmaxf(k2[2], k2[3])) * pieces;
+                const int32_t e = max(-(root_exponent(sum4(norm)) + root_exponent(k_norm) +
+                                        (int32_t)__builtin_ceilf(fminf(gain, 1e6f))), -120);
+                bi += (float)(15 + e);
+                if (g == 0) {
+                    lds.row[wave][col] = __builtin_amdgcn_exp2f(bi);
+                    lds.last[wave][col] = __builtin_ldexpf(a.scale, -15 - e);
+                }
+                __builtin_amdgcn_wave_barrier();
+                row = *(const f32x4 *)&lds.row[wave][4 * g];
+            } else {
+                row = *(const f32x4 *)&lds.eb[16 * it + 4 * g];
+            }
 #pragma unroll
             for (int j = 0; j < EV; ++j) {
-                const float grow = __is_same(Type, Fp16) ? lds.grow[j / CW] : 1.0f;
+                const float grow = fp16 ? lds.grow[j / CW] : 1.0f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     o[j][r] *= row[r] * grow;
             }
-            const float bi = lds.b[16 * it + col];
             for (int half = 0; 2 * half <= it; ++half) {
                 u32x4 w = {0, 0, 0, 0};   // scores of token 16 it + col with 8 keys of the half
 #pragma unroll
@@ -811,7 +898,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                     const f32x4 bj = *(const f32x4 *)&lds.b[16 * jt + 4 * g];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        x[r] *= a.scale * __builtin_amdgcn_exp2f(bi - bj[r]);
+                        x[r] *= (fp16 ? 1.0f : a.scale) * __builtin_amdgcn_exp2f(bi - bj[r]);
                         x[r] = jt < it || 4 * g + r <= col ? x[r] : 0.0f;
                     }
                     w[2 * k] = pack2(Type(), x[0], x[1]);
@@ -820,6 +907,14 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
 #pragma unroll
                 for (int j = 0; j < EV; ++j)
                     o[j] = mfma(Type(), w, lds.v[half][j][lane], o[j]);
+            }
+            if constexpr (fp16) {
+                const f32x4 last = *(const f32x4 *)&lds.last[wave][4 * g];
+#pragma unroll
+                for (int j = 0; j < EV; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        o[j][r] *= last[r];
             }
             if (odd) {
                 rare();
@@ -955,7 +1050,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
 template <class Type, int DK, int DV, bool OUT>
 __global__ __launch_bounds__(kSegmentThreads, 2) void linear_chunk_kernel(LinearArgs a, Cuts cuts)
 {
-    __shared__ __align__(16) ChunkLds<DK, DV, OUT> lds;
+    __shared__ __align__(16) ChunkLds<Type, DK, DV, OUT> lds;
     Segment seg;
     if (!find_segment(a, cuts, blockIdx.y, !OUT, &seg))
         return;
