@@ -1,13 +1,38 @@
-"""Linear attention over operands of every size: what a type's range could lose. Bounds are mixer_oracle's."""
+"""Linear attention over operands of every size: what a type's range or a rounding term could lose.
+
+Bounds of single elements are mixer_oracle's. Those of a whole state are of its norm: with b the largest sum of
+log decays that stands in an exponent, a factor e^b is off by b half steps of float32 (its exponent's rounding) and
+two of the exponential, its product with v by one, what the terms of the type leave by one, and sums by fewer than
+twelve, as they are rounded at random: (b + 16) 2^-24. (One bfloat16 term fewer is off by 40 of those.)
+"""
+import math
+
 import pytest
 import torch
 
+import mixer_oracle as mo
 import weight_only_int4_w4a16_amd as w
 from test_gpu_linear_attention import Linear
 
 pytestmark = pytest.mark.gpu
 
-FP16 = torch.float16
+BF16, FP16 = torch.bfloat16, torch.float16
+
+
+def check(x, out, state, exponent=0.0):
+    """Elements by their bounds, each sequence's state also by its norm."""
+    assert bool(out.isfinite().all()) and bool(state.isfinite().all())
+    x.check(out, state)
+    at = x.lead
+    for s, n in enumerate(x.lens):
+        g = x.g[at:at + n] if x.g.dim() == 2 else x.g.expand(n, x.H)
+        S0 = torch.zeros(state.shape[1:]).double() if x.state is None else x.state[s].double()
+        _, S, _, _ = mo.linear(x.q[at:at + n].double(), x.k[at:at + n].double(), x.v[at:at + n].double(), g.double(),
+                               S0, x.scale)
+        for h in range(x.H):
+            off = float((state[s, h].cpu().double() - S[h]).norm() / S[h].norm())
+            assert off <= (exponent + 16) * mo.F32, f"sequence {s}, head {h}: state off by {off:.3g} of its norm"
+        at += n
 
 
 @pytest.mark.parametrize("n", [1, 40, 200])
@@ -23,7 +48,7 @@ def test_scores_past_the_range_of_float16(n, size, v_size):
     x.v[:, :, 0] = 0
     x.state *= v_size * size
     out, state = x.run(scale=x.scale)
-    x.check(out, state)
+    check(x, out, state)
     if n == 40:   # token by token, in float32
         q, k, v, g, s = (t.cuda() for t in (x.q, x.k, x.v, x.g, x.state))
         rows = torch.cat([w.linear_attention_step(q[t:t + 1], k[t:t + 1], v[t:t + 1], g[t:t + 1], s, scale=x.scale)
@@ -39,4 +64,54 @@ def test_rows_of_every_size():
     x.k = (x.k.float() * (2.0 ** -(8 + t % 3))[:, None, None]).to(FP16)
     x.v = (x.v.float() * 1000).to(FP16)
     x.scale = 1.0
-    x.check(*x.run(scale=1.0))
+    check(x, *x.run(scale=1.0))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("amp", [1e-2, 1e-3, 1e-4])
+@pytest.mark.parametrize("n", [200, 700])
+def test_small_queries_and_keys(dtype, amp, n):
+    x = Linear([n], 2, 1, 128, 128, dtype, seed=n, rate=0.02, initial=False)
+    x.q, x.k = ((t.float() * amp).to(dtype) for t in (x.q, x.k))
+    x.scale = 0.1 / amp ** 2
+    check(x, *x.run(scale=x.scale))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("n", [200, 700])
+def test_small_values(dtype, n):
+    """Values among float16's subnormals, beside keys that bring them up; then large ones."""
+    torch.manual_seed(n)
+    x = Linear([n], 2, 1, 128, 128, dtype, seed=n, rate=0.02, initial=False, amp=30.0)
+    x.v = (x.v.float() / 30 * 1e-6).to(dtype)
+    check(x, *x.run())
+    x.v[150:] = (torch.randn(x.v[150:].shape) * 100).to(dtype)
+    x.q = (x.q.float() * 1e-3).to(dtype)
+    check(x, *x.run())
+    x.v = x.v.flip(0)
+    check(x, *x.run())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("n,growth,cleared", [(64, 0.1, ()), (130, 0.3, ()), (1500, 0.01, ()), (2500, 0.02, ()),
+                                              (700, 0.05, (100, 300, 520))])
+def test_growth(dtype, n, growth, cleared):
+    """Positive log decays: factors of e^6 to e^50 stand before values of hundreds."""
+    torch.manual_seed(n)
+    x = Linear([n], 2, 1, 64, 64, dtype, seed=n)
+    x.v = (x.v.float() * 200).to(dtype)
+    x.g = growth * (0.9 + 0.2 * torch.rand(x.g.shape))
+    x.g[list(cleared)] = -math.inf
+    total = n * growth
+    x.scale = 0.1 * math.exp(-total)
+    check(x, *x.run(scale=x.scale), exponent=1.1 * total * 1.443)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("lens", [[200], [1500, 70], [3, 64, 129]])
+def test_digits_of_states(dtype, lens):
+    """States to float32's digits: every term of the products that return them counts."""
+    x = Linear(lens, 2, 1, 128, 128, dtype, seed=sum(lens), rate=0.02, initial=False)
+    check(x, *x.run())
+    x = Linear(lens, 2, 1, 128, 128, dtype, seed=sum(lens), rate=0.0)
+    check(x, *x.run())

@@ -142,6 +142,13 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 // positive; the power of two that brings this bound to 2^15 goes with e^{b_i} and is taken back from the
 // query's sum. Scores below 2^-29 of the bound lose digits. (Costs 0.3 us of 43 for nine sequences of up to 300 tokens.)
 //
+// So has e^{b_63 - b_j} v_j (decays of a whole segment may stand there), and its second term, 2^-11 of the first,
+// is soon among the subnormals. Column by column the state is therefore held as 2^up times itself, with the
+// power that brings the chunk's largest |v| times the largest e^{b_63 - b_j} to 2^15: 22 bits down to 2^-17 of
+// that, 11 down to 2^-29. The factor goes with the decay of the state; a sum over chunks keeps its smallest
+// one. (Terms that only get 2^11 times their remainders, against k times 2^-11, put that among the subnormals for
+// k below 0.1.) With it nine sequences of up to 300 tokens take 44.4 us instead of 43.3.
+//
 // One segment per sequence needs one launch. Longer ones take three: what each segment adds to a state
 // (k and v read once), the states before every segment and after the last (a running sum over segments),
 // then the outputs of all segments side by side.
@@ -154,6 +161,7 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 constexpr int kChunk = 64;
 constexpr int kSegmentThreads = 256;
 constexpr float kNone = -104.0f;
+constexpr int kMostUp = 100;
 constexpr int kWaveSeqs = 64;   // up to here every wave finds its segment by itself
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -186,10 +194,6 @@ __device__ __forceinline__ float high(Bf16, uint32_t w) { return __builtin_bit_c
 __device__ __forceinline__ float low(Fp16, uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[0]; }
 __device__ __forceinline__ float high(Fp16, uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[1]; }
 
-// What rounding to `r` leaves of x. A float16 remainder is kept 2^11 times as large, so that it does not
-// fall among the subnormals, and meets k times 2^-11.
-__device__ __forceinline__ float left(Bf16, float x, float r) { return x - r; }
-__device__ __forceinline__ float left(Fp16, float x, float r) { return (x - r) * 2048.0f; }
 // Rounds a pair and keeps what that leaves in its place, for the next term. The remainder goes by the bits
 // that the product gets: left to itself, the compiler rounds v * d once for one use and twice (float32
 // first) for the other.
@@ -198,21 +202,31 @@ __device__ __forceinline__ uint32_t take(Type t, float &a, float &b)
 {
     uint32_t both = pack2(t, a, b);
     asm volatile("" : "+v"(both));
-    a = left(t, a, low(t, both));
-    b = left(t, b, high(t, both));
+    a -= low(t, both);
+    b -= high(t, both);
     return both;
 }
-// As many values of the type as hold a float32's digits.
+// As many values of the type as hold a float32's digits, or nearly.
 template <class Type>
 struct Terms {
     static constexpr int count = __is_same(Type, Bf16) ? 3 : 2;
 };
-__device__ __forceinline__ u32x4 for_rest(Bf16, u32x4 k) { return k; }
-__device__ __forceinline__ u32x4 for_rest(Fp16, u32x4 k)
+
+// The larger magnitudes (without signs) of two pairs of float16 values; NaN is above infinity.
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t larger_pair(uint32_t x, uint32_t y)
 {
-    return __builtin_bit_cast(u32x4, __builtin_bit_cast(f16x8, k) * (_Float16)(1.0f / 2048.0f));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, x),
+                                                                  __builtin_bit_cast(u16x2, y)));
 }
-// Sum over the four lanes that share lane % 16.
+// The same over the four lanes that share lane % 16; and a sum.
+__device__ __forceinline__ uint32_t larger_pair4(uint32_t x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = larger_pair(r[0], r[1]);
+    const auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return larger_pair(s[0], s[1]);
+}
 __device__ __forceinline__ float sum4(float v)
 {
     uint32_t x = __builtin_bit_cast(uint32_t, v);
@@ -233,6 +247,7 @@ __device__ __forceinline__ int32_t root_exponent(float sum)
 {
     return (__builtin_amdgcn_frexp_expf(fmaxf(sum, 0x1p-21f)) + 1) >> 1;
 }
+__device__ __forceinline__ float power(int32_t e) { return __builtin_ldexpf(1.0f, e); }
 
 // Rows of a chunk as a buffer: `n` of them, `ld` elements apart and `width` long. What lies past the last
 // row's end reads as zeros and isn't written, so that a chunk's loads need no branches: where one comes
@@ -287,14 +302,10 @@ struct Count {
 // Keeps a branch that is hardly ever taken a branch, rather than selects on the way past it.
 __device__ __forceinline__ void rare() { asm volatile("; rare"); }
 
-// acc plus both values times zero: NaN from the first one on that is not finite.
-__device__ __forceinline__ float times_zero(Bf16, uint32_t w, float acc)
+// acc plus both bfloat16 values times zero: NaN from the first one on that is not finite.
+__device__ __forceinline__ float times_zero(uint32_t w, float acc)
 {
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), bf16x2{(__bf16)0.0f, (__bf16)0.0f}, acc, false);
-}
-__device__ __forceinline__ float times_zero(Fp16, uint32_t w, float acc)
-{
-    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), f16x2{(_Float16)0.0f, (_Float16)0.0f}, acc, false);
 }
 
 // The sign's place is set for a value that is not finite (its exponent field, plus one unit of it).
@@ -328,12 +339,6 @@ __device__ __forceinline__ float wave_max(float v)
     x = max(r[0], r[1]);
     const auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
     return __builtin_bit_cast(float, max(s[0], s[1]));
-}
-
-// The power of two that brings values up to `most` below 2^15, for float16.
-__device__ __forceinline__ float fit(float most)
-{
-    return __builtin_ldexpf(1.0f, min(15 - __builtin_amdgcn_frexp_expf(most), 126));
 }
 
 template <int CTRL, int ROWS>
@@ -542,9 +547,10 @@ struct ChunkLds {
     u32x4 v[2][DV / 16][64];                          // second operands: half of the chunk, column
     u32x4 s[OUT ? DK / 32 : 1][OUT ? DV / 16 : 1][64];   // and the state's: pair of tiles, column
     float b[kChunk], eb[kChunk], ed[kChunk];          // per token: b (log2), scale e^b (bfloat16), e^(b_63 - b)
-    float grow[kSegmentThreads / 64];                 // a wave's part of s is smaller by this
-    // float16: sums of squares of k; a wave's queries' factors, before and after the products with v
-    float squares[kSegmentThreads / 64];
+    // float16: by how much a wave's part of s is smaller; sums of squares of k; largest magnitudes of v (half
+    // of the chunk, column in pairs); a wave's queries' factors, before and after the products with v
+    float grow[kSegmentThreads / 64], squares[kSegmentThreads / 64];
+    uint32_t most_v[fp16 ? 2 : 1][16][DV / 32];
     float row[fp16 && OUT ? kSegmentThreads / 64 : 1][16], last[fp16 && OUT ? kSegmentThreads / 64 : 1][16];
     // What is not finite, in even and odd chunks: whether, first token of k, dims of k, first tokens of v
     uint32_t odd[2], bad_token[2], bad_dims[2][DK / 32], bad_column[2][DV];
@@ -603,6 +609,12 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             for (int c = 0; c < CW; ++c)
                 s[j][c][r] = x[c];
         }
+
+    // float16: s is held as 2^up times itself, column by column
+    int32_t up[CW];
+#pragma unroll
+    for (int c = 0; c < CW; ++c)
+        up[c] = OUT ? 0 : kMostUp;
 
     u32x4 q[contractions];   // dims (Dk / 4) g .. + Dk / 4 of token 16 it + col
     u32x4 kn[loads];
@@ -671,8 +683,12 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
         const float whole_chunk = __builtin_amdgcn_exp2f((float)end);
         const double behind = OUT ? end : whole + end;
         whole += end;
-        float gain = 0.0f;   // float16: the largest b_i - b_j of a token, which is 0 without growth
-        if constexpr (fp16 && OUT) {
+        // float16: the largest e^(b_63 - b), as a power of two, and a token's largest e^(b_i - b_j). Without
+        // growth they are that of the last token, and 1.
+        int32_t most_ed = 0;
+        float gain = 0.0f;
+        if constexpr (fp16) {
+            double least = end;
             if (__ballot(gc > 0.0f)) {
                 rare();
                 float x = (float)b;
@@ -682,7 +698,10 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                         x = fminf(x, o);
                 }
                 gain = __shfl((float)b - x, 16 * it + col);
+                least = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
             }
+            const float x = fminf(fmaxf((float)(behind - least), -1e6f), 1e6f);
+            most_ed = __builtin_amdgcn_readfirstlane((int32_t)__builtin_ceilf(x));
         }
         const int parity = chunks_left & 1;
         __syncthreads();   // the previous chunk has been read
@@ -702,31 +721,44 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                 lds.bad_column[parity ^ 1][i] = kChunk;
         }
         float squares = 0.0f;
-        auto add_up = [&]() {
+        uint32_t most_v[CW] = {};
+        auto sizes = [&]() {
             squares = 0.0f;
 #pragma unroll
             for (int i = 0; i < loads; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     squares = add_squares(kn[i][e], squares);
+#pragma unroll
+            for (int x = 0; x < CW; ++x) {
+                most_v[x] = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    most_v[x] = larger_pair(most_v[x], vn[e][x] & 0x7FFF7FFFu);
+            }
         };
-        float seen = 0.0f;   // 0, or NaN where something is not finite
+        bool finite;
         if constexpr (fp16) {
-            add_up();
-            seen = squares * 0.0f;
+            sizes();
+            finite = squares < INFINITY;
+#pragma unroll
+            for (int x = 0; x < CW; ++x)
+                finite = finite && !(odd_bits(Type(), most_v[x]) & 0x80008000u);
         } else {
+            float seen = 0.0f;   // 0, or NaN where something is not finite
 #pragma unroll
             for (int i = 0; i < loads; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    seen = times_zero(Type(), kn[i][e], seen);
+                    seen = times_zero(kn[i][e], seen);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int x = 0; x < CW; ++x)
+                    seen = times_zero(vn[e][x], seen);
+            finite = seen == seen;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-#pragma unroll
-            for (int x = 0; x < CW; ++x)
-                seen = times_zero(Type(), vn[e][x], seen);
-        if (__ballot(seen != seen)) {
+        if (__ballot(!finite)) {
             rare();
             lds.odd[parity] = 1;
 #pragma unroll
@@ -758,12 +790,18 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                         atomicMin(&lds.bad_column[parity][d + 1], row);
                 }
             if constexpr (fp16)
-                add_up();
+                sizes();
         }
         if constexpr (fp16) {
             squares = wave_max(squares);
             if (lane == 0)
                 lds.squares[wave] = squares;
+#pragma unroll
+            for (int x = 0; x < CW; ++x) {
+                const uint32_t most = larger_pair4(most_v[x]);
+                if (g == 0)
+                    lds.most_v[v_half][col][v_first / 2 + x] = most;
+            }
         }
 #pragma unroll
         for (int i = 0; i < loads; ++i)
@@ -779,17 +817,24 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             lds.v[v_half][v_first + 2 * x][lane] = v0;
             lds.v[v_half][v_first + 2 * x + 1][lane] = v1;
         }
+        int32_t s_exponent = 0;   // float16: all of s is below 2^this
         if (OUT) {
-            float shrink = 1.0f;   // bfloat16 needs none
-            if constexpr (__is_same(Type, Fp16)) {
+            float shrink[CW];
+#pragma unroll
+            for (int c = 0; c < CW; ++c)
+                shrink[c] = 1.0f;   // bfloat16 needs none
+            if constexpr (fp16) {
                 float most = 0.0f;
 #pragma unroll
-                for (int j = 0; j < EK; ++j)
+                for (int c = 0; c < CW; ++c) {
+                    float x = 0.0f;
 #pragma unroll
-                    for (int c = 0; c < CW; ++c) {
-                        most = larger(most, s[j][c][0], s[j][c][1]);
-                        most = larger(most, s[j][c][2], s[j][c][3]);
+                    for (int j = 0; j < EK; ++j) {
+                        x = larger(x, s[j][c][0], s[j][c][1]);
+                        x = larger(x, s[j][c][2], s[j][c][3]);
                     }
+                    most = larger(most, __builtin_ldexpf(x, -up[c]), 0.0f);
+                }
                 most = wave_max(most);
                 if (!(most < INFINITY)) {   // the finite ones' scale
                     rare();
@@ -800,14 +845,18 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                         for (int r = 0; r < 4; ++r)
 #pragma unroll
                             for (int c = 0; c < CW; ++c) {
-                                const float x = fabsf(s[j][c][r]);
+                                const float x = fabsf(__builtin_ldexpf(s[j][c][r], -up[c]));
                                 most = x < INFINITY && x > most ? x : most;
                             }
                     most = wave_max(most);
                 }
-                shrink = fit(most);
+                s_exponent = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(most));
+                const int32_t to = min(15 - s_exponent, 100);
+#pragma unroll
+                for (int c = 0; c < CW; ++c)
+                    shrink[c] = power(min(to - up[c], 127));
                 if (lane == 0)
-                    lds.grow[wave] = 1.0f / shrink;
+                    lds.grow[wave] = power(-to);
             }
 #pragma unroll
             for (int p = 0; p < WK; ++p)
@@ -816,7 +865,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                     u32x4 x;
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        x[r] = pack2(Type(), s[2 * p][c][r] * shrink, s[2 * p + 1][c][r] * shrink);
+                        x[r] = pack2(Type(), s[2 * p][c][r] * shrink[c], s[2 * p + 1][c][r] * shrink[c]);
                     lds.s[p][CW * wave + c][lane] = x;
                 }
         }
@@ -826,7 +875,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                 if constexpr (!fp16)
                     lds.eb[lane] = a.scale * __builtin_amdgcn_exp2f((float)b);
             }
-            lds.ed[lane] = lane < n ? __builtin_amdgcn_exp2f((float)(behind - b)) : 0.0f;
+            lds.ed[lane] = lane < n ? __builtin_amdgcn_exp2f((float)(behind - b - most_ed)) : 0.0f;
         }
         __syncthreads();
         odd = __builtin_amdgcn_readfirstlane(lds.odd[parity]) != 0;
@@ -948,14 +997,41 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
         if (OUT)
             fetch_q(t + kChunk);
         __builtin_amdgcn_sched_barrier(0);
+        // s after the chunk's decay. float16: and with the power of two that brings this chunk's largest
+        // e^(b_63 - b) |v| of the column just below 2^15 (a sum over chunks: the largest so far), unless s itself
+        // would pass 2^120 with it; v meets what of that e^(b_63 - b) does not.
+        float fade[CW], v_up[CW];
+        bool same = true;
 #pragma unroll
-        for (int j = 0; j < EK; ++j)
+        for (int c = 0; c < CW; ++c)
+            fade[c] = whole_chunk;
+        if constexpr (fp16) {
+            uint32_t most_v[(CW + 1) / 2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int x = 0; x < (CW + 1) / 2; ++x)
+                most_v[x] = larger_pair(lds.most_v[0][col][CW * wave / 2 + x], lds.most_v[1][col][CW * wave / 2 + x]);
+            const int32_t room = 120 - s_exponent - max((int32_t)__builtin_ceilf(fminf((float)end, 1e6f)), 0);
 #pragma unroll
-                for (int c = 0; c < CW; ++c)
-                    s[j][c][r] = OUT ? s[j][c][r] * whole_chunk : s[j][c][r];
+            for (int c = 0; c < CW; ++c) {
+                const float most = (CW * wave + c) & 1 ? high(Type(), most_v[c / 2]) : low(Type(), most_v[c / 2]);
+                const int32_t want = most > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(most) - most_ed : kMostUp;
+                const int32_t now = max(OUT ? min(min(want, kMostUp), min(room, up[c] + 100)) : min(want, up[c]), -140);
+                fade[c] = OUT ? __builtin_amdgcn_exp2f(fminf((float)end + (float)(now - up[c]), 126.0f))
+                              : power(now - up[c]);
+                same = same && now == up[c];
+                up[c] = now;
+                v_up[c] = power(now + most_ed);
             }
+        }
+        if (OUT || (fp16 && __ballot(!same))) {
+#pragma unroll
+            for (int j = 0; j < EK; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int c = 0; c < CW; ++c)
+                        s[j][c][r] *= fade[c];
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             constexpr int terms = REST ? Terms<Type>::count : Terms<Type>::count - 1;
@@ -968,7 +1044,13 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                 const f32x2 d = *(const f32x2 *)&lds.ed[32 * half + 16 * (e / 2) + 4 * g + 2 * (e & 1)];
 #pragma unroll
                 for (int c = 0; c < CW; ++c) {
-                    float v0 = low(Type(), x[0][c][e]) * d[0], v1 = high(Type(), x[0][c][e]) * d[1];
+                    float v0 = low(Type(), x[0][c][e]), v1 = high(Type(), x[0][c][e]);
+                    if constexpr (fp16) {
+                        v0 *= v_up[c];
+                        v1 *= v_up[c];
+                    }
+                    v0 *= d[0];
+                    v1 *= d[1];
 #pragma unroll
                     for (int i = 0; i < terms; ++i)
                         x[i][c][e] = take(Type(), v0, v1);
@@ -1000,10 +1082,6 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                 }
 #pragma unroll
                 for (int i = 0; i < terms; ++i) {
-                    if (i == 1) {
-                        k0 = for_rest(Type(), k0);
-                        k1 = for_rest(Type(), k1);
-                    }
 #pragma unroll
                     for (int c = 0; c < CW; ++c) {
                         s[2 * w][c] = mfma(Type(), k0, x[i][c], s[2 * w][c]);
@@ -1040,7 +1118,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             float x[CW];
 #pragma unroll
             for (int c = 0; c < CW; ++c)
-                x[c] = s[j][c][r];
+                x[c] = fp16 ? __builtin_ldexpf(s[j][c][r], -up[c]) : s[j][c][r];
             __builtin_memcpy(__builtin_assume_aligned(to + state_at + (int64_t)(EK * r + j) * DV, 4 * CW), x, 4 * CW);
         }
     if (!OUT && tid == 0)
