@@ -115,3 +115,18 @@ def test_digits_of_states(dtype, lens):
     check(x, *x.run())
     x = Linear(lens, 2, 1, 128, 128, dtype, seed=sum(lens), rate=0.0)
     check(x, *x.run())
+
+
+@pytest.mark.parametrize("dtype,n,size,growth", [
+    (BF16, 60, 1e30, 80.0), (BF16, 130, 1e30, 80.0), (BF16, 700, 1e30, 80.0), (BF16, 700, 1e37, 20.0),
+    (FP16, 130, 1e37, 20.0), (FP16, 700, 1e37, 20.0),
+])
+@pytest.mark.parametrize("g0", [-math.inf, -1e4])
+def test_cleared_before_growth(dtype, n, size, growth, g0):
+    """A decay of zero counts as such when the ones after it grow."""
+    x = Linear([n], 2, 2, 64, 64, dtype, seed=n)
+    x.g = torch.full((n, 2), growth / (n - 1))
+    x.g[0] = g0
+    x.k[:-1] = 0
+    x.state *= size
+    x.check(*x.run())

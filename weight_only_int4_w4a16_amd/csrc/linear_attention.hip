@@ -134,8 +134,9 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 // outputs of 32768 bfloat16 tokens are off by 2.35e-3 of their norm (2.57e-3 with one bfloat16 value,
 // 1.66e-3 by their own rounding alone; S in float16 as well would make it 2.0e-3 for another 20 us of 400),
 // states by 5e-7. Decays are summed in float64 over a chunk; the scores' take the sums in float32, off by
-// 2^-24 of their size. A log decay below -104 counts as that: e^-104 is zero in float32, and so a state
-// that is cleared by -inf costs its neighbours few digits.
+// 2^-24 of their size. A log decay below -193 counts as that: with growth by up to e^88, float32's
+// largest, behind it that is e^-105, zero in float32, and so a state that is cleared by -inf costs its neighbours
+// few digits.
 //
 // Scores have more range than float16. Those of a query are bounded by its norm, the chunk's largest norm of a
 // key (from sums of squares, which also show what is not finite) and the largest e^{b_i - b_j} where decays are
@@ -160,7 +161,7 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 // wave, which are alone on their SIMD.
 constexpr int kChunk = 64;
 constexpr int kSegmentThreads = 256;
-constexpr float kNone = -104.0f;
+constexpr float kNone = -193.0f;
 constexpr int kMostUp = 100;
 constexpr int kWaveSeqs = 64;   // up to here every wave finds its segment by itself
 
