@@ -130,3 +130,12 @@ def test_cleared_before_growth(dtype, n, size, growth, g0):
     x.k[:-1] = 0
     x.state *= size
     x.check(*x.run())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_large_first_state(dtype):
+    """A first state of 1e30 beside ordinary tokens, which decays away."""
+    x = Linear([500, 70], 2, 2, 64, 128, dtype, seed=9, rate=2.0)
+    x.state *= 1e30
+    x.scale = 1e-30
+    check(x, *x.run(scale=x.scale), exponent=700.0)

@@ -138,6 +138,8 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 // largest, behind it that is e^-105, zero in float32, and so a state that is cleared by -inf costs its neighbours
 // few digits.
 //
+// The scale comes last: with e^{b_i} it could leave float32's range where the output does not.
+//
 // Scores have more range than float16. Those of a query are bounded by its norm, the chunk's largest norm of a
 // key (from sums of squares, which also show what is not finite) and the largest e^{b_i - b_j} where decays are
 // positive; the power of two that brings this bound to 2^15 goes with e^{b_i} and is taken back from the
@@ -547,7 +549,7 @@ struct ChunkLds {
     uint16_t k[kChunk][DK + 8];
     u32x4 v[2][DV / 16][64];                          // second operands: half of the chunk, column
     u32x4 s[OUT ? DK / 32 : 1][OUT ? DV / 16 : 1][64];   // and the state's: pair of tiles, column
-    float b[kChunk], eb[kChunk], ed[kChunk];          // per token: b (log2), scale e^b (bfloat16), e^(b_63 - b)
+    float b[kChunk], eb[kChunk], ed[kChunk];          // per token: b (log2), e^b (bfloat16), e^(b_63 - b)
     // float16: by how much a wave's part of s is smaller; sums of squares of k; largest magnitudes of v (half
     // of the chunk, column in pairs); a wave's queries' factors, before and after the products with v
     float grow[kSegmentThreads / 64], squares[kSegmentThreads / 64];
@@ -874,7 +876,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
             if (OUT) {
                 lds.b[lane] = (float)b;
                 if constexpr (!fp16)
-                    lds.eb[lane] = a.scale * __builtin_amdgcn_exp2f((float)b);
+                    lds.eb[lane] = __builtin_amdgcn_exp2f((float)b);
             }
             lds.ed[lane] = lane < n ? __builtin_amdgcn_exp2f((float)(behind - b - most_ed)) : 0.0f;
         }
@@ -948,7 +950,7 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                     const f32x4 bj = *(const f32x4 *)&lds.b[16 * jt + 4 * g];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        x[r] *= (fp16 ? 1.0f : a.scale) * __builtin_amdgcn_exp2f(bi - bj[r]);
+                        x[r] *= __builtin_amdgcn_exp2f(bi - bj[r]);
                         x[r] = jt < it || 4 * g + r <= col ? x[r] : 0.0f;
                     }
                     w[2 * k] = pack2(Type(), x[0], x[1]);
@@ -958,14 +960,14 @@ __device__ __forceinline__ void run_segment(const LinearArgs &a, const Cuts &cut
                 for (int j = 0; j < EV; ++j)
                     o[j] = mfma(Type(), w, lds.v[half][j][lane], o[j]);
             }
-            if constexpr (fp16) {
-                const f32x4 last = *(const f32x4 *)&lds.last[wave][4 * g];
+            f32x4 last = {a.scale, a.scale, a.scale, a.scale};
+            if constexpr (fp16)
+                last = *(const f32x4 *)&lds.last[wave][4 * g];
 #pragma unroll
-                for (int j = 0; j < EV; ++j)
+            for (int j = 0; j < EV; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        o[j][r] *= last[r];
-            }
+                for (int r = 0; r < 4; ++r)
+                    o[j][r] *= last[r];
             if (odd) {
                 rare();
 #pragma unroll
