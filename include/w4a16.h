@@ -341,8 +341,8 @@ w4a16_status_t w4a16_paged_kv_write(const void *k, int64_t ldk, int64_t hsk, con
  *   16 query heads of a KV head, the 128-position units that a whole row of its table could have sum up
  *   to less than 2^31: B * heads * ceil(Hq / heads / 16) * (ceil(max_pages * page_size / 128) + 1).
  *   workspace: w4a16_paged_attention_workspace bytes. Products and sums are held in float32; the
- *   probabilities enter their product with the values rounded to `type`. Repeated calls give
- *   identical bits.
+ *   probabilities enter their product with the values rounded to `type` (float16: 11 bits down to 2^-29 of
+ *   the largest, and nothing below 2^-40 of it). Repeated calls give identical bits.
  */
 w4a16_status_t w4a16_paged_attention(const void *q, int64_t ldq, int64_t hsq, int32_t type,
                                      const w4a16_paged_cache_t *cache, const int32_t *page_table,

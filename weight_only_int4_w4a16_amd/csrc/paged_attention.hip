@@ -41,6 +41,12 @@ constexpr int kThreads = 256, kWaves = 4, kTile = 32, kUnit = kWaves * kTile;
 constexpr int kMaxWorkers = 512;   // work-groups of a launch; each leaves at most two pieces
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
+// Weights are 2^(score - reference), scores in powers of two, and the reference is this much below the largest
+// score so far: float16 weights then keep their 11 bits down to 2^-29 of the largest one. (With 0 they lost them
+// from 2^-14 on, and 18 nats behind a position of little value all others were gone from the sum.)
+template <class Type>
+constexpr float kHeadroom = __is_same(Type, Fp16) ? 15.0f : 0.0f;
+
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
@@ -529,7 +535,7 @@ __global__ __launch_bounds__(kThreads, E4M3 || D <= 128 ? 2 : 1) void attention_
 #pragma unroll
             for (int e = 1; e < 8; ++e)
                 m = fmaxf(m, x[e]);
-            m = fmaxf(max4(m), top);
+            m = fmaxf(max4(m) - kHeadroom<Type>, top);
             const float ref = m == -INFINITY ? 0.0f : m;   // nothing seen yet: every weight is 0
             const float fade = __builtin_amdgcn_exp2f(top - ref);
             top = m;
@@ -539,7 +545,7 @@ __global__ __launch_bounds__(kThreads, E4M3 || D <= 128 ? 2 : 1) void attention_
                 x[e] = __builtin_amdgcn_exp2f(x[e] - ref);
                 total += x[e];
             }
-            // The probabilities, at most 1, are rounded to the activations' type for the matrix
+            // The weights, at most 2^kHeadroom, are rounded to the activations' type for the matrix
             // product (their sum is not): what a float32 product would cost is 8 times the MFMA time.
             u32x4 p;
 #pragma unroll
