@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import mixer_oracle as mo
-from test_gpu_paged_attention import Paged
+from test_gpu_paged_attention import Paged, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,16 @@ def test_lengths_and_windows_at_float16():
         out, sums = p.run(0.09, window=window)
         p.check(out, sums, 0.09, window)
     assert math.isinf(float(sums[0, 0])) and bool((out[0] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("window", [0, 1, 500, 2 ** 31 - 1])
+def test_lengths_below_zero(dtype, window):
+    """Lengths down to the least integer are requests without positions, with any window."""
+    p = Paged([5, 40, 9], 4, 2, 64, 16, dtype, seed=12)
+    out, sums = p.run(0.125, window=window, lens=ints([-2 ** 31, 40, -1]))
+    for b in (0, 2):
+        assert bool((out[b] == 0).all()) and bool((sums[b] == -math.inf).all())
+    p.lens = [0, 40, 0]
+    p.rows = [[x[:n] for x, n in zip(rows, p.lens)] for rows in p.rows]
+    p.check(out, sums, 0.125, window)

@@ -122,9 +122,9 @@ struct Span {
 
 __device__ __forceinline__ Span span_of(const AttentionArgs &a, int b)
 {
-    const int32_t len = a.lens[b];
+    const int32_t len = max(a.lens[b], 0);
     Span s;
-    s.n = max(min(len, a.max_pages * a.page_size), 0);
+    s.n = min(len, a.max_pages * a.page_size);
     s.lo = a.window ? max(len - a.window, 0) : 0;
     s.base = s.lo & ~(kUnit - 1);
     s.units = s.n > s.lo ? ((uint32_t)(s.n - s.base) + kUnit - 1) / kUnit : 1;
