@@ -387,7 +387,8 @@ w4a16_status_t w4a16_linear_attention(const void *q, int64_t ldq, int64_t hsq, c
                                       int64_t workspace_bytes, hipStream_t stream);
 
 /* Bytes of workspace for w4a16_linear_attention (host only); 0 where none is needed, -1 where the
- * arguments are out of range. */
+ * arguments are out of range. Never less for more tokens or sequences, so what is made for the largest
+ * prompts does for all others with these heads. */
 int64_t w4a16_linear_attention_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk,
                                          int32_t Dv);
 

@@ -1240,37 +1240,52 @@ int32_t segment_length(int32_t T, int32_t H)
 
 int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
 
+// No call of at most T tokens has more whole segments than this: segments of L tokens, which are 128 to 512
+// and, rounded down, T H / 256 at least, are fewer than 258 / H; those of 512 to 4096, T H / 512 at least, at most
+// 513 / H; and so on. It never falls as T rises, which T / segment_length(T) does.
+int32_t most_whole(int32_t T, int32_t H)
+{
+    if (T <= 256)
+        return H <= 258 ? T / 256 : 0;
+    const int32_t a = T / 128 < 258 / H ? T / 128 : 258 / H, b = T / 512 < 513 / H ? T / 512 : 513 / H;
+    const int32_t c = T / 4096 < 16384 ? T / 4096 : 16384, ab = a > b ? a : b;
+    return ab > c ? ab : c;
+}
+
 // A sequence of several segments has x + 1 <= 2x of them, x the whole segments before its last token,
 // and all such x sum up to at most T / L. One sequence without bounds has T / L and one, if that.
-Cuts cuts_of(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk, int32_t Dv, float *work, int64_t *bytes)
+void count_slots(Cuts &c, int32_t whole, int32_t num_seqs)
 {
-    Cuts c;
-    c.L = segment_length(T, H);
-    const int32_t whole = T / c.L;
     c.inner = num_seqs == 1 ? whole + (whole > 0) : 2 * whole;
     c.slots = c.inner + (num_seqs < whole ? num_seqs : whole);
+}
+
+// Places in the workspace; returns its size.
+int64_t place(Cuts &c, int32_t num_seqs, int32_t H, int32_t Dk, int32_t Dv, float *work)
+{
     const int64_t states = (int64_t)c.slots * H * Dk * Dv * 4, decays = round16((int64_t)c.slots * H * 4);
     const int64_t maps = num_seqs > kWaveSeqs ? round16(3 * ((int64_t)num_seqs + 1) * 4) : 0;
     c.states = work;
     c.decays = (float *)((char *)work + states);
     c.maps = (int32_t *)((char *)c.decays + decays);
-    *bytes = states + decays + maps;
-    return c;
+    return states + decays + maps;
 }
 
 }  // namespace
 
 int64_t linear_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk, int32_t Dv)
 {
-    int64_t bytes;
-    cuts_of(T, num_seqs, H, Dk, Dv, nullptr, &bytes);
-    return bytes;
+    Cuts c{};
+    count_slots(c, most_whole(T, H), num_seqs);
+    return place(c, num_seqs, H, Dk, Dv, nullptr);
 }
 
 hipError_t launch_linear(const LinearArgs &a, int, hipStream_t stream)
 {
-    int64_t bytes;
-    const Cuts c = cuts_of(a.T, a.B, a.H, a.Dk, a.Dv, a.work, &bytes);
+    Cuts c;
+    c.L = segment_length(a.T, a.H);
+    count_slots(c, a.T / c.L, a.B);
+    place(c, a.B, a.H, a.Dk, a.Dv, a.work);
     return a.type ? linear_typed<Fp16>(a, c, stream) : linear_typed<Bf16>(a, c, stream);
 }
 

@@ -382,7 +382,8 @@ def _mixed(out, v, dev: int, stream):
 
 
 def linear_attention_workspace(q: torch.Tensor, v: torch.Tensor, num_seqs: int = 1) -> torch.Tensor:
-    """Scratch memory for linear_attention over the tokens of q and v in `num_seqs` sequences."""
+    """Scratch memory for linear_attention over the tokens of q and v in `num_seqs` sequences, or over fewer
+    tokens or sequences."""
     need = _library().w4a16_linear_attention_workspace(q.shape[0], num_seqs, v.shape[1], q.shape[2],
                                                        v.shape[2])
     return torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
