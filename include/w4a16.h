@@ -68,7 +68,8 @@ typedef enum {
     W4A16_ERR_UNSUPPORTED_DEVICE = 5, /* no current HIP device, or it is not gfx950           */
     W4A16_ERR_LAUNCH = 6,             /* the HIP runtime refused the kernel launch            */
     W4A16_ERR_BAD_TYPE = 7,           /* a type code names no type the call takes             */
-    W4A16_ERR_WORKSPACE = 8           /* the workspace is smaller than the call needs         */
+    W4A16_ERR_WORKSPACE = 8,          /* the workspace is smaller than the call needs         */
+    W4A16_ERR_OVERLAP = 9             /* what a call writes shares memory with its operands   */
 } w4a16_status_t;
 
 /*
@@ -263,7 +264,8 @@ w4a16_status_t w4a16_describe_moe_batched_plan(int32_t M, int64_t N, int64_t K, 
  *
  * Strides are in elements. Offsets into caches, states and activations are computed in 64 bits.
  * A workspace is scratch device memory of the caller (16-byte aligned, contents irrelevant before
- * and after a call); it may be reused by the next call on the same stream.
+ * and after a call); it may be reused by the next call on the same stream. What a call writes shares no
+ * memory with its other operands, unless that is allowed below.
  * ------------------------------------------------------------------------------------------- */
 
 typedef enum { W4A16_BF16 = 0, W4A16_FP16 = 1, W4A16_E4M3 = 2 } w4a16_type_t;
@@ -299,7 +301,9 @@ typedef struct {
  *   that position, or -1 where the row has no page for it; both are -1 from the last token on.
  *   counts int32[2]: tokens (sum of n_b) and pages taken (more than num_free: the list was too
  *   short; more tokens than max_tokens: the last ones have no slot).
- *   Sums saturate at 2^31 - 1. The call is idempotent while its inputs do not change.
+ *   Sums saturate at 2^31 - 1. The call is idempotent while its inputs do not change. To carry the lengths
+ *   on, copy seq_lens to ctx_lens after the call: in place (and any other operand that is written and
+ *   shares memory with one) it is refused with W4A16_ERR_OVERLAP.
  *   page_table int32[B] rows of row_stride >= max_pages entries, max_pages >= 1; 1 <= B <= 16384;
  *   num_free, max_tokens >= 0 (their pointers may be null at 0); 1 <= page_size <= 65536.
  */

@@ -389,6 +389,7 @@ const char *w4a16_status_string(w4a16_status_t status)
     case W4A16_ERR_LAUNCH: return "kernel launch failed";
     case W4A16_ERR_BAD_TYPE: return "type not taken by this call";
     case W4A16_ERR_WORKSPACE: return "workspace too small";
+    case W4A16_ERR_OVERLAP: return "operands share memory that one of them writes";
     }
     return "unknown status";
 }

@@ -20,6 +20,18 @@ bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 bool strided8(int64_t a, int64_t b) { return a % 8 == 0 && b % 8 == 0; }
 w4a16_status_t done(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_LAUNCH; }
 
+// `count` int32 values from `p` share memory with rows of `width` values, `stride` apart, from `base`.
+bool in_rows(const int32_t *p, int64_t count, const int32_t *base, int64_t rows, int64_t stride, int64_t width)
+{
+    const int64_t lo = ((int64_t)(uintptr_t)p - (int64_t)(uintptr_t)base) / 4, hi = lo + count;
+    const int64_t row = lo < width ? 0 : (lo - width) / stride + 1;   // the first one that ends behind lo
+    return p && count > 0 && row < rows && row * stride < hi;
+}
+bool shared(const int32_t *p, int64_t count, const int32_t *q, int64_t other)
+{
+    return q && other > 0 && in_rows(p, count, q, 1, other, other);
+}
+
 // What every call asks of a cache; `type` is that of the activations.
 w4a16_status_t check_cache(const w4a16_paged_cache_t *c, int32_t type)
 {
@@ -88,6 +100,16 @@ w4a16_status_t w4a16_page_tables(const int32_t *ctx_lens, const int32_t *new_len
             return W4A16_ERR_MISALIGNED;
     if (!current_device())
         return W4A16_ERR_UNSUPPORTED_DEVICE;
+    // Work-groups read the inputs while others write: nothing that is written may be read, or written twice.
+    const struct { const int32_t *p; int64_t n; } own[] = {{seq_lens, B}, {cu_new, (int64_t)B + 1}, {counts, 2},
+        {slot_map, max_tokens}, {positions, max_tokens}, {ctx_lens, B}, {new_lens, B}, {free_pages, num_free}};
+    for (int i = 0; i < 8; ++i) {
+        if (in_rows(own[i].p, own[i].n, page_table, B, row_stride, max_pages))
+            return W4A16_ERR_OVERLAP;
+        for (int j = i + 1; i < 5 && j < 8; ++j)
+            if (shared(own[i].p, own[i].n, own[j].p, own[j].n))
+                return W4A16_ERR_OVERLAP;
+    }
     PageTablesArgs a{ctx_lens, new_lens, page_table, free_pages, seq_lens, cu_new, slot_map, positions,
                      counts, row_stride, B, max_pages, num_free, page_size, max_tokens};
     return done(launch_page_tables(a, stream));
