@@ -43,6 +43,7 @@ class HybridDecoder:
                                v_scale=torch.full((kv_heads,), 0.02, device="cuda"))
         self.table = torch.full((requests, -(-longest // page_size)), -1, dtype=torch.int32, device="cuda")
         self.free = torch.randperm(pages, device="cuda", generator=self.gen).to(torch.int32)
+        self.rank = torch.arange(pages, device="cuda")
         self.lens = torch.zeros(requests, dtype=torch.int32, device="cuda")
         self.state = torch.zeros(requests, heads, dim, dim, device="cuda")
 
@@ -72,13 +73,19 @@ class HybridDecoder:
             rows.append(w.moe_down_combine(*self.down[layer], ids[t], weights[t], h))
         return torch.stack(rows).to(torch.bfloat16)
 
+    def place(self, new, max_tokens):
+        """Pages and slots of a step's new tokens; lengths and the free list move on, all on the device."""
+        step = w.page_tables(self.lens, new, self.table, self.free, self.page_size, max_tokens=max_tokens)
+        self.lens.copy_(step.seq_lens)
+        at = self.rank + step.counts[1]   # what is left, -1 (no page) behind it
+        self.free.copy_(torch.where(at < self.free.numel(), self.free[at.clamp(max=self.free.numel() - 1)], -1))
+        return step
+
     def forward(self, tokens, new_lens):
         """Logits of every new token: `tokens` holds new_lens[b] of request b, one after the other."""
         T, heads, kv, dim = tokens.shape[0], self.heads, self.kv_heads, self.dim
         new = torch.tensor(new_lens, dtype=torch.int32, device="cuda")
-        step = w.page_tables(self.lens, new, self.table, self.free, self.page_size, max_tokens=T)
-        pages = int(step.counts[1])
-        self.free, self.lens = self.free[pages:].contiguous(), step.seq_lens
+        step = self.place(new, T)
         row = torch.repeat_interleave(torch.arange(len(new_lens), device="cuda"), new.long())
         x = self.embed[tokens]
 

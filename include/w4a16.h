@@ -301,9 +301,11 @@ typedef struct {
  *   that position, or -1 where the row has no page for it; both are -1 from the last token on.
  *   counts int32[2]: tokens (sum of n_b) and pages taken (more than num_free: the list was too
  *   short; more tokens than max_tokens: the last ones have no slot).
- *   Sums saturate at 2^31 - 1. The call is idempotent while its inputs do not change. To carry the lengths
- *   on, copy seq_lens to ctx_lens after the call: in place (and any other operand that is written and
- *   shares memory with one) it is refused with W4A16_ERR_OVERLAP.
+ *   Sums saturate at 2^31 - 1. The call is idempotent while its inputs do not change.
+ *   The list is read from its start and the lengths are not moved on. For the next step copy seq_lens to
+ *   ctx_lens (in place it is refused, W4A16_ERR_OVERLAP, as is all else that is written and shares memory
+ *   with another operand) and move the list on by counts[1]: entry i + counts[1] to place i, and -1, which is
+ *   no page, past its end. Both can be done on the device, so a captured loop needs no host.
  *   page_table int32[B] rows of row_stride >= max_pages entries, max_pages >= 1; 1 <= B <= 16384;
  *   num_free, max_tokens >= 0 (their pointers may be null at 0); 1 <= page_size <= 65536.
  */

@@ -205,14 +205,18 @@ def page_tables_buffers(batch: int, max_tokens: int, device=None, stream=None) -
 def page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, page_table: torch.Tensor,
                 free_pages: torch.Tensor, page_size: int, max_tokens: Optional[int] = None,
                 out: Optional[PageTables] = None, stream=None) -> PageTables:
-    """Page tables and slot maps of one step from the requests' lengths, without a host round trip.
+    """Page tables and slot maps of one step from the requests' lengths, made on the device.
 
     Request b holds ctx_lens[b] cached tokens and gets new_lens[b] new ones (int32 [B]). The pages that it
     needs beyond those it has are taken from free_pages (int32) in order of the requests and written
     into its row of page_table (int32 [B, max_pages], in place). Returns, with the new tokens of all
     requests one after the other: the lengths after the step, the requests' first tokens, each
     token's slot and position (-1 past the last token, slot -1 where there is no page), and the
-    counts of tokens and pages taken. Give max_tokens or `out`."""
+    counts of tokens and pages taken. Give max_tokens or `out`.
+
+    The list is read from its start, and the lengths are not moved on. For the next step copy seq_lens to
+    ctx_lens and drop counts[1] pages from the list, on the device (no host round trip, so in a graph as well):
+    `at = torch.arange(n) + counts[1]; free.copy_(torch.where(at < n, free[at.clamp(max=n - 1)], -1))`."""
     if out is not None and max_tokens is None and stream is None:
         _library()
         if _short(_binding.page_tables(ctx_lens, new_lens, page_table, free_pages, page_size, *out),
