@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 from typing import NamedTuple, Optional
 
 import torch
@@ -92,6 +93,8 @@ def _need(t, name: str, types, ndim: int, dev: int) -> int:
     if isinstance(t, torch.Tensor) and t.dtype in types and t.dim() == ndim:
         at = t.get_device()
         if at >= 0 and (dev < 0 or at == dev):
+            if max(t.shape, default=0) >= 2 ** 31 and t.dtype != torch.uint8:   # a workspace may be longer
+                raise ValueError(f"{name} is too long: {tuple(t.shape)}")
             return at
     _refuse(t, name, types, ndim, dev)
 
@@ -107,6 +110,14 @@ def _refuse(t, name: str, types, ndim: int, dev: int):
     if at < 0:
         raise ValueError(f"{name} must be on a GPU")
     raise ValueError(f"{name} is on GPU {at}, the other operands on GPU {dev}")
+
+
+def _int32(x, name: str) -> int:
+    """x as an int; ctypes would pass 2**32 + 16 on as 16."""
+    x = operator.index(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
 
 
 def _flat(t, name: str, types, ndim: int, dev: int) -> int:
@@ -222,6 +233,7 @@ def page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, page_table: torc
         if _short(_binding.page_tables(ctx_lens, new_lens, page_table, free_pages, page_size, *out),
                   "w4a16_page_tables"):
             return out
+    page_size = _int32(page_size, "page_size")
     dev = _flat(ctx_lens, "ctx_lens", _I32, 1, -1)
     _flat(new_lens, "new_lens", _I32, 1, dev)
     _need(page_table, "page_table", _I32, 2, dev)
@@ -314,6 +326,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                                            _factor(scale, q), window, out, lse, workspace),
                   "w4a16_paged_attention"):
             return out
+    window = _int32(window, "window")
     dev = _need(q, "q", _HALF, 3, -1)
     c = _cache_of(k_cache, v_cache, k_scale, v_scale, q.dtype, dev)
     _need(page_table, "page_table", _I32, 2, dev)
