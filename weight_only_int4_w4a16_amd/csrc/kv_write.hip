@@ -8,9 +8,9 @@
 // first takes 23.7.
 //
 // The e4m3 code is that of the float32 quotient x / scale. With r = 1 / scale correctly rounded,
-// q0 = x r and q = q0 + (x - q0 scale) r (two fused operations) is that quotient exactly wherever
+// q0 = x r and q = q0 - (q0 scale - x) r (two fused operations) is that quotient exactly wherever
 // nothing over- or underflows (Markstein), for one division per thread; scales far from 1 take the
-// division itself.
+// division itself. (With x - q0 scale, which is +0 for -0, a zero would lose its sign.)
 #include "mixers.h"
 #include "mixer_types.h"
 
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvWriteArgs a, PageO
             if (near) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const float v = Type::f(in.v[e]), q0 = v * r, q = fmaf(fmaf(-q0, scale, v), r, q0);
+                    const float v = Type::f(in.v[e]), q0 = v * r, q = fmaf(-fmaf(q0, scale, -v), r, q0);
                     f[e] = clamp448(fabsf(q0) < 1e30f ? q : q0);   // infinities and NaN as they are
                 }
             } else {
