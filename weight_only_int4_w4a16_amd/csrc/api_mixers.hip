@@ -226,10 +226,9 @@ w4a16_status_t w4a16_linear_attention(const void *q, int64_t ldq, int64_t hsq, c
         return W4A16_ERR_MISALIGNED;
     if (workspace_bytes < need)
         return W4A16_ERR_WORKSPACE;
-    const DeviceInfo *dev = current_device();
-    if (!dev)
+    if (!current_device())
         return W4A16_ERR_UNSUPPORTED_DEVICE;
-    return done(launch_linear(a, dev->cus, stream));
+    return done(launch_linear(a, stream));
 }
 
 w4a16_status_t w4a16_linear_attention_step(const void *q, int64_t ldq, int64_t hsq, const void *k,
@@ -249,12 +248,11 @@ w4a16_status_t w4a16_linear_attention_step(const void *q, int64_t ldq, int64_t h
         return st;
     if (B < 0 || B > kMaxGrid || num_states < 0 || (!slots && num_states < B))
         return W4A16_ERR_BAD_SHAPE;
-    const DeviceInfo *dev = current_device();
-    if (!dev)
+    if (!current_device())
         return W4A16_ERR_UNSUPPORTED_DEVICE;
     if (B == 0)
         return W4A16_OK;
-    return done(launch_linear_step(a, dev->cus, stream));
+    return done(launch_linear_step(a, stream));
 }
 
 }  // extern "C"

@@ -1280,7 +1280,7 @@ int64_t linear_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk, int
     return place(c, num_seqs, H, Dk, Dv, nullptr);
 }
 
-hipError_t launch_linear(const LinearArgs &a, int, hipStream_t stream)
+hipError_t launch_linear(const LinearArgs &a, hipStream_t stream)
 {
     Cuts c;
     c.L = segment_length(a.T, a.H);
@@ -1289,7 +1289,7 @@ hipError_t launch_linear(const LinearArgs &a, int, hipStream_t stream)
     return a.type ? linear_typed<Fp16>(a, c, stream) : linear_typed<Bf16>(a, c, stream);
 }
 
-hipError_t launch_linear_step(const LinearArgs &a, int, hipStream_t stream)
+hipError_t launch_linear_step(const LinearArgs &a, hipStream_t stream)
 {
     a.type ? step_typed<Fp16>(a, stream) : step_typed<Bf16>(a, stream);
     return hipGetLastError();

@@ -59,8 +59,8 @@ struct LinearArgs {
 hipError_t launch_page_tables(const PageTablesArgs &a, hipStream_t stream);
 hipError_t launch_kv_write(const KvWriteArgs &a, int cus, hipStream_t stream);
 hipError_t launch_attention(const AttentionArgs &a, int cus, hipStream_t stream);
-hipError_t launch_linear(const LinearArgs &a, int cus, hipStream_t stream);
-hipError_t launch_linear_step(const LinearArgs &a, int cus, hipStream_t stream);
+hipError_t launch_linear(const LinearArgs &a, hipStream_t stream);
+hipError_t launch_linear_step(const LinearArgs &a, hipStream_t stream);
 
 int64_t attention_workspace(int32_t Hq, int32_t heads, int32_t dim);
 // Most units of work of one request and head.
