@@ -378,10 +378,10 @@ int64_t w4a16_paged_attention_workspace(int32_t Hq, int32_t heads, int32_t dim);
  *   Dk, Dv in {64, 128}; H % Hk == 0; 0 <= T <= 2^31 - 65; 1 <= num_seqs <= 16384; H <= 32767.
  *   States, decays and sums are held in float32 or more; within the library the operands of matrix
  *   products are rounded to `type`, those that reach state_out as a sum of such values (24 bits of
- *   three bfloat16, 22 of two float16: those down to 2^-17 of a v's column's largest |v| times the
- *   largest decay factor among 64 tokens, 11 bits down to 2^-29). float16 scores keep their 11 bits, whatever the size of q and k, down to
- *   2^-29 of the norm of q_t times the largest norm of a k (and times the largest decay factor, where
- *   decays are positive) among 64 tokens.
+ *   three bfloat16, 22 of two float16: those for terms down to 2^-17 of a column's largest |v| times the
+ *   largest decay factor among the tokens that are summed with it, 11 bits down to 2^-29). float16 scores
+ *   keep their 11 bits, whatever the size of q and k, down to 2^-29 of the norm of q_t times the largest norm
+ *   of a k (and times the largest decay factor, where decays are positive) among 64 tokens.
  */
 w4a16_status_t w4a16_linear_attention(const void *q, int64_t ldq, int64_t hsq, const void *k,
                                       int64_t ldk, int64_t hsk, const void *v, int64_t ldv,

@@ -2,10 +2,10 @@
 // divided by the head's scale and rounded to e4m3. Memory-bound: 2 bytes read and 2 or 1 written per
 // value. A thread moves the values of one 16-byte store at a time (8, or 16 as e4m3) and stays with its
 // piece of the row, eight work-groups per CU going over the tokens: head, dims and scale are worked out
-// once, and the slot's page by a multiplication. 16411 tokens of 8 heads of 128: e4m3 22.1 us (4.6 TB/s),
-// bfloat16 28.3 us (4.8); 100000 tokens bfloat16 154 us (5.3 TB/s). With the divisions of a flat index
-// per piece the first took 25 to 28 us; with 4 work-groups per CU the last takes 159 us, with 16 the
-// first takes 23.7.
+// once, and the slot's page by a multiplication. 16411 tokens of 8 heads of 128 as e4m3: 19.7 us (5.1 TB/s);
+// 100000 tokens: e4m3 120 us (5.1), bfloat16 155 us (5.3). With the divisions of a flat index per piece the
+// first took 25 to 28 us where this took 22; with 4, 8 and 16 work-groups per CU the last takes 162, 155 and 156 us,
+// the others differ less.
 //
 // The e4m3 code is that of the float32 quotient x / scale. With r = 1 / scale correctly rounded,
 // q0 = x r and q = q0 - (q0 scale - x) r (two fused operations) is that quotient exactly wherever

@@ -16,8 +16,8 @@ namespace {
 // Few heads and requests leave CUs idle, so below 128 of them a work-group owns 32 columns; from there on
 // a whole state, with streaming loads and stores (a model's other layers push it out of every cache
 // before the next token). Graphs of 48 layers of 32 heads of 128 x 128, us per layer, split / whole /
-// whole streaming: 1 request 3.1 / 3.8 / 4.1, 2 requests 3.6 / 4.1 / 4.3, 4 requests 5.9 / 6.2 / 4.7,
-// 16 requests 16.8 / 15.8 / 12.0, 256 requests 218 / 215 / 186 (5.8 TB/s).
+// whole streaming: 1 request 3.1 / 3.8 / 4.1, 2 requests 3.6 / 4.1 / 4.3, 4 requests 5.9 / 6.3 / 4.8,
+// 16 requests 16.8 / 15.9 / 12.4, 256 requests 215 / 211 / 183 (5.9 TB/s).
 constexpr int kStepThreads = 256;
 
 template <class Type, int DK, int DV, int CV, bool STREAM>
@@ -143,7 +143,8 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 // Scores have more range than float16. Those of a query are bounded by its norm, the chunk's largest norm of a
 // key (from sums of squares, which also show what is not finite) and the largest e^{b_i - b_j} where decays are
 // positive; the power of two that brings this bound to 2^15 goes with e^{b_i} and is taken back from the
-// query's sum. Scores below 2^-29 of the bound lose digits. (Costs 0.3 us of 43 for nine sequences of up to 300 tokens.)
+// query's sum. Scores below 2^-29 of the bound lose digits. (Costs 0.3 us of 43 for nine sequences of up to 300
+// tokens.)
 //
 // So has e^{b_63 - b_j} v_j (decays of a whole segment may stand there), and its second term, 2^-11 of the first,
 // is soon among the subnormals. Column by column the state is therefore held as 2^up times itself, with the
@@ -156,11 +157,11 @@ void step_typed(const LinearArgs &a, hipStream_t stream)
 // (k and v read once), the states before every segment and after the last (a running sum over segments),
 // then the outputs of all segments side by side.
 //
-// What bounds it (128 x 128, 32 heads of 32768 bfloat16 tokens, 398 us in all): the outputs move 1.07 GB in
-// 240 to 255 us (4.2 to 4.5 TB/s, where a copy of 4 GiB reaches 4.7); the segments' sums read 0.54 GB in 173 us, with
-// the vector units busy for 47 and the matrix units for 29 % of it (the three terms). A short sequence
-// is bound by the chain of its chunks, 4.5 us each: two barriers, and between them the products of a
-// wave, which are alone on their SIMD.
+// What bounds it (128 x 128, 32 heads of 32768 bfloat16 tokens, 402 us in all): the outputs move 1.07 GB in
+// 240 to 255 us (4.2 to 4.5 TB/s, where a copy of 4 GiB reaches 4.7); the segments' sums read 0.54 GB in 171 us, with
+// the vector units busy for 44 and the matrix units for 32 % of it (the three terms). A short sequence
+// is bound by the chain of its chunks, 4.4 us each (float16 4.8): two barriers, and between them the products of a
+// wave, which are alone on their SIMD; before them stand 8.6 us of launch and states read and written.
 constexpr int kChunk = 64;
 constexpr int kSegmentThreads = 256;
 constexpr float kNone = -193.0f;
@@ -1217,13 +1218,13 @@ hipError_t linear_typed(const LinearArgs &a, const Cuts &c, hipStream_t stream)
     return a.Dv == 64 ? linear_of<Type, 128, 64>(a, c, stream) : linear_of<Type, 128, 128>(a, c, stream);
 }
 
-// Tokens per segment, as many as leave one segment per CU of a 256-CU device and at least 128; past 512
-// tokens as many as leave two. A segment's state is written and read once (128 KB per head of 128 x 128,
-// against 1.5 KB per token), so longer ones move less and shorter ones end sooner. Measured, us for
-// tokens x heads of 128 x 128, bfloat16, with segments of 128 / 256 / 512: 700 x 8 26 / 38 / 64,
-// 2048 x 8 31 / 41 / 66, 1024 x 32 41 / 44 / 68, 2048 x 32 66 / 54 / 70, 8192 x 8 84 / 65 / 75; of 512
-// and 1024: 8192 x 32 118 and 134; of 1024, 2048 and 4096: 32768 x 32 446, 400 and 469. Up to 256 tokens
-// in all, where a cut can only halve them, it costs more than it gives (200 x 16: 24 and 22).
+// Tokens per segment, as many as leave one segment per CU (256 of them: the workspace's size may be asked for
+// where there is no device) and at least 128; past 512 tokens as many as leave two. A segment's state is
+// written and read once (128 KB per head of 128 x 128, against 1.5 KB per token), so longer ones move less and
+// shorter ones end sooner. Measured, us for tokens x heads of 128 x 128, bfloat16, with segments of 128 / 256 / 512: 700 x 8 26 / 39 / 65,
+// 2048 x 8 33 / 42 / 67, 1024 x 32 41 / 44 / 68, 2048 x 32 67 / 55 / 71, 8192 x 8 83 / 64 / 75; of 512
+// and 1024: 8192 x 32 125 and 137; of 1024, 2048 and 4096: 32768 x 32 439, 400 and 472. Up to 256 tokens
+// in all, where a cut can only halve them, it costs more than it gives (200 x 16: 25 and 22).
 int32_t segment_length(int32_t T, int32_t H)
 {
     const int64_t all = (int64_t)T * H;

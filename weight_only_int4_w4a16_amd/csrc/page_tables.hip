@@ -8,9 +8,10 @@
 // A new page is taken from the free list by whoever needs it (the table's writer and the slot's), so
 // no value written by this launch is read by it.
 //
-// Latency bounds it: 5.6 us for one token of each of 8 requests, 8.9 us for 500 prompts of 108 thousand
-// tokens in all (0.9 MB), against about 2.5 us for an empty launch; the rest is three dependent trips to
-// memory (lengths, then table entry or free page, then the stores), with the sums' barriers between.
+// Latency bounds it: 5.6 us for one token of each of 8 requests, 9.1 us for 500 prompts of 108 thousand
+// tokens in all (0.9 MB), against about 2.5 us for an empty launch; the rest is dependent trips to memory
+// (lengths; those of the request that was found, once more; table entry or free page; the stores), with the
+// sums' barriers between.
 #include "mixers.h"
 
 namespace w4a16 {

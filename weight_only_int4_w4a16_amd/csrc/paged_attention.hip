@@ -22,12 +22,13 @@
 //
 // The loads of a tile's V and of the next tile's K are in flight during the arithmetic: 8 to 16 KB
 // for each of 8 waves per CU (bfloat16, dim 128). More work-groups per CU (3 or 4, with fewer registers
-// each) were slower. They are streaming loads: nothing is read twice, and kept lines only push others
-// out (64 ragged requests of up to 8192 positions 171 -> 152 us before the last steps).
+// each) are slower (64 ragged requests of up to 8192 positions 152 -> 175 and 269 us).
+// They are streaming loads: nothing is read twice, and kept lines only push others out (the same requests
+// 171 -> 152 us before the last steps).
 //
 // Measured, 8 KV heads of 128: those 64 requests, 8 query heads to a KV head, 144 us in all, 140 of them
 // here (6.15 TB/s, where a plain streaming read of 4 GiB reaches 6.3); 48 requests of 5000 positions as e4m3 27 us
-// here and 5 us joining; one request of 131000 positions 95 and 9 us (5.6 TB/s); one of 1100
+// here and 5 us joining; one request of 131000 positions 96 and 8 us (5.6 TB/s); one of 1100
 // positions 5.8 and 4.4 us, which is latency: lengths, page table, rows, the join of four waves, and all
 // that once more for the second launch.
 #include "mixers.h"
