@@ -259,7 +259,7 @@ w4a16_status_t w4a16_describe_moe_batched_plan(int32_t M, int64_t N, int64_t K, 
 
 /* ---------------------------------------------------------------------------------------------
  * Token mixers of a decode or prompt step: page tables, the paged key-value cache, attention of
- * one new token over it, and linear attention. They stand between the weight products above: the
+ * one new token over it, linear attention and the gated delta rule. They stand between the weight products above: the
  * pages name neither, so formats and readings here are this library's own.
  *
  * Strides are in elements. Offsets into caches, states and activations are computed in 64 bits.
@@ -268,7 +268,7 @@ w4a16_status_t w4a16_describe_moe_batched_plan(int32_t M, int64_t N, int64_t K, 
  * memory with its other operands, unless that is allowed below.
  * ------------------------------------------------------------------------------------------- */
 
-typedef enum { W4A16_BF16 = 0, W4A16_FP16 = 1, W4A16_E4M3 = 2 } w4a16_type_t;
+typedef enum { W4A16_BF16 = 0, W4A16_FP16 = 1, W4A16_E4M3 = 2, W4A16_INT8 = 3 } w4a16_type_t;
 
 /*
  * A paged key-value cache: `num_pages` pages of `page_size` slots, each slot one row of `dim`
@@ -414,6 +414,111 @@ w4a16_status_t w4a16_linear_attention_step(const void *q, int64_t ldq, int64_t h
                                            int32_t type, float scale, const float *state_in,
                                            float *state_out, void *out, int64_t ldo, int64_t hso,
                                            hipStream_t stream);
+
+/*
+ * The gated delta rule over packed sequences (the form for prompts): linear attention whose state first gives up
+ * what it holds for the new key,
+ *   S_t = e^{g_t} S_{t-1} + k_t u_t^T,   u_t = beta_t (v_t - e^{g_t} S_{t-1}^T k_t),   o_t = scale * q_t^T S_t.
+ *   beta float: beta_t of head h at beta[t * ldb + h * hsb] (ldb from 0 to 2^24 - 1). Keys of norm 1 and beta from
+ *   0 to 2 are meant: with beta |k|^2 above 2 states may grow from token to token.
+ *   All else as for w4a16_linear_attention: layouts, strides, decays, cu_seqlens, states (state_out == state_in is
+ *   allowed), limits; and num_seqs * H <= 2^26.
+ *   States, decays and sums are held in float32 or more, and the operands of all products that reach a state
+ *   as sums of three bfloat16 values (24 bits). What reaches the outputs only is rounded to one bfloat16 (the
+ *   scores) or two (16 bits; float16 inputs: two everywhere). A k, v, beta or decay that is not finite (a decay
+ *   of -inf is fine) makes NaN of what it reaches: for v its column, else all columns, from its token on. Repeated
+ *   calls give identical bits.
+ */
+w4a16_status_t w4a16_delta_rule(const void *q, int64_t ldq, int64_t hsq, const void *k, int64_t ldk, int64_t hsk,
+                                const void *v, int64_t ldv, int64_t hsv, const float *log_decay, int64_t ldg,
+                                int64_t hsg, const float *beta, int64_t ldb, int64_t hsb,
+                                const int32_t *cu_seqlens, int32_t num_seqs, int32_t T, int32_t Hk, int32_t H,
+                                int32_t Dk, int32_t Dv, int32_t type, float scale, const float *state_in,
+                                float *state_out, void *out, int64_t ldo, int64_t hso, void *workspace,
+                                int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace for w4a16_delta_rule (host only), -1 where the arguments are out of range. Never less for
+ * more tokens or sequences. */
+int64_t w4a16_delta_rule_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk, int32_t Dv, int32_t type);
+
+/*
+ * The recurrent form of w4a16_delta_rule for one new token of each of B requests, as
+ * w4a16_linear_attention_step is of w4a16_linear_attention: states by slots, in place or not. All
+ * arithmetic is float32.
+ */
+w4a16_status_t w4a16_delta_rule_step(const void *q, int64_t ldq, int64_t hsq, const void *k, int64_t ldk,
+                                     int64_t hsk, const void *v, int64_t ldv, int64_t hsv, const float *log_decay,
+                                     int64_t ldg, int64_t hsg, const float *beta, int64_t ldb, int64_t hsb,
+                                     const int32_t *slots, int32_t num_states, int32_t B, int32_t Hk, int32_t H,
+                                     int32_t Dk, int32_t Dv, int32_t type, float scale, const float *state_in,
+                                     float *state_out, void *out, int64_t ldo, int64_t hso, hipStream_t stream);
+
+/*
+ * A paged key-value cache in 8 bits with a scale for each block of tokens and head: pages, slots and strides
+ * as in w4a16_paged_cache_t, and a page's slots cut into blocks of `block` tokens. A value is its code times
+ * the float scale of its block and head, at scale[page * stride[0] + (slot / block) * stride[1] + head * stride[2]]
+ * (slot: within the page; keys and values have scales of their own).
+ *   type: W4A16_INT8 (codes -127 to 127) or W4A16_E4M3 (OCP float8, largest 448).
+ *   block 16, 32, 48 or 64 and page_size a multiple of it; dim 64, 96, 128, 192 or 256; num_pages, page_size,
+ *   heads as in w4a16_paged_cache_t. k, v 16-byte aligned, their strides multiples of 16, slot strides 0 to
+ *   2^24 - 1. Scale strides are free.
+ * The scales are written by w4a16_quantized_kv_write; before that, codes and scales may be anything.
+ */
+typedef struct {
+    void *k, *v;
+    int64_t k_stride[3], v_stride[3];               /* page, slot, head */
+    float *k_scale, *v_scale;
+    int64_t k_scale_stride[3], v_scale_stride[3];   /* page, block, head */
+    int32_t num_pages, page_size, heads, dim, block;
+    int32_t type;
+} w4a16_quantized_cache_t;
+
+/*
+ * Quantises T tokens' keys and values into such a cache: slot slot_map[t] receives k[t] and v[t] (rows and
+ * strides as for w4a16_paged_kv_write; a slot outside the cache is skipped). Tokens whose slots follow each
+ * other in a block are one run. With Q = 127 or 448 and amax the largest |x| of the run's rows of a head,
+ *   s' = max(float(amax / Q), 2^-126)            where the run starts at the block's first slot,
+ *   s' = max(float(amax / Q), 2^-126, s)         otherwise, s the scale that the block has,
+ *   code = x / s' to the nearest code, ties to even (of the exact quotient),
+ * and where s' > s in the second case the block's other slots keep their values as far as they can: their codes
+ * become code * s / s', rounded in the same way. A run that starts a block drops what the block held: codes of
+ * slots behind it are left as they are and stand for nothing.
+ *   So a sequence is written from its first position on, in any number of calls, and may be taken back to any
+ *   length and continued. Runs of one call lie in different blocks (two of them in one leave it undefined, and
+ *   touch nothing else).
+ *   Where a run's row holds a value that is not finite, the scale becomes NaN and the run's codes zero: the whole
+ *   block and head then reads as NaN, until it is started anew.
+ *   0 <= T; k, v of `type` W4A16_BF16 or W4A16_FP16, 16-byte aligned, strides multiples of 8.
+ */
+w4a16_status_t w4a16_quantized_kv_write(const void *k, int64_t ldk, int64_t hsk, const void *v, int64_t ldv,
+                                        int64_t hsv, int32_t T, int32_t type, const int32_t *slot_map,
+                                        const w4a16_quantized_cache_t *cache, hipStream_t stream);
+
+/*
+ * Reads slots back: k[t] and v[t] receive the values of slot slot_map[t], code * scale rounded once to `type`
+ * W4A16_BF16 or W4A16_FP16 (nearest even), or zeros for a slot outside the cache. Slots may repeat.
+ */
+w4a16_status_t w4a16_quantized_kv_read(const w4a16_quantized_cache_t *cache, const int32_t *slot_map, int32_t T,
+                                       int32_t type, void *k, int64_t ldk, int64_t hsk, void *v, int64_t ldv,
+                                       int64_t hsv, hipStream_t stream);
+
+/*
+ * w4a16_paged_attention over such a cache: the same operands, masks, limits and results. Products and sums are
+ * held in float32; the probabilities, times the scale of their value, enter their product with the codes as
+ * float16 (11 bits down to 2^-29 of the largest, and nothing below 2^-40 of it), for both types of activations;
+ * bfloat16 queries enter theirs as float16 times a power of two (exact down to 2^-32 of a head's largest
+ * magnitude). Scales of blocks without a position that is read may be anything. A scale that is NaN makes NaN of
+ * the requests and heads that read a position of its block (of keys: lse as well).
+ */
+w4a16_status_t w4a16_quantized_attention(const void *q, int64_t ldq, int64_t hsq, int32_t type,
+                                         const w4a16_quantized_cache_t *cache, const int32_t *page_table,
+                                         int64_t row_stride, int32_t max_pages, const int32_t *seq_lens, int32_t B,
+                                         int32_t Hq, float scale, int32_t window, void *out, int64_t ldo,
+                                         int64_t hso, float *lse, void *workspace, int64_t workspace_bytes,
+                                         hipStream_t stream);
+
+/* Bytes of workspace for w4a16_quantized_attention, as w4a16_paged_attention_workspace. */
+int64_t w4a16_quantized_attention_workspace(int32_t Hq, int32_t heads, int32_t dim);
 
 /* Static, never-NULL description of a status code. */
 const char *w4a16_status_string(w4a16_status_t status);

@@ -13,7 +13,8 @@ Tensor conventions:
            out [topk, N]
 
 The token mixers between the weight products (page tables, paged cache, paged attention, linear
-attention) are in mixers.py and reached from here as well.
+attention) are in mixers.py, the gated delta rule in delta.py, the 8-bit cache with a scale for each block
+and head in quantized.py; all are reached from here as well.
 
 If libw4a16.so has not been built, every call raises ImportError; there is no fallback.
 """
@@ -32,7 +33,8 @@ __all__ = ["gemv", "gemv_batched", "moe_gemv", "moe_gemv_batched", "moe_gemv_swi
            "library", "LIB_PATH", "GROUP_SIZE", "MAX_BATCH",
            "PageTables", "page_tables", "page_tables_buffers", "paged_kv_write", "paged_attention",
            "paged_attention_workspace", "linear_attention", "linear_attention_workspace",
-           "linear_attention_step"]
+           "linear_attention_step", "delta_rule", "delta_rule_workspace", "delta_rule_step",
+           "quantized_kv_write", "quantized_kv_read", "quantized_attention", "quantized_attention_workspace"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw4a16.so")
 GROUP_SIZE = 128
@@ -399,3 +401,6 @@ def stream_read(buf: torch.Tensor, nbytes: int, out: torch.Tensor, blocks: int, 
 from .mixers import (PageTables, linear_attention, linear_attention_step,  # noqa: E402
                      linear_attention_workspace, page_tables, page_tables_buffers, paged_attention,
                      paged_attention_workspace, paged_kv_write)
+from .delta import delta_rule, delta_rule_step, delta_rule_workspace  # noqa: E402
+from .quantized import (quantized_attention, quantized_attention_workspace, quantized_kv_read,  # noqa: E402
+                        quantized_kv_write)

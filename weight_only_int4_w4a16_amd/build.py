@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libw4a16.so")
 SOURCES = ["kernels.hip", "kernels3.hip", "quantize.hip", "stream_probe.hip", "api.hip", "plan.cpp",
            "page_tables.hip", "kv_write.hip", "paged_attention.hip", "linear_attention.hip",
-           "api_mixers.hip"]
+           "delta_rule.hip", "quantized_kv.hip", "quantized_attention.hip", "api_mixers.hip"]
 BINDING = os.path.join(PKG, "_binding.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

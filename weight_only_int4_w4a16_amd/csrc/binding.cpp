@@ -20,6 +20,11 @@ decltype(&w4a16_paged_kv_write) g_kv_write;
 decltype(&w4a16_paged_attention) g_attention;
 decltype(&w4a16_linear_attention) g_linear;
 decltype(&w4a16_linear_attention_step) g_step;
+decltype(&w4a16_delta_rule) g_delta;
+decltype(&w4a16_delta_rule_step) g_delta_step;
+decltype(&w4a16_quantized_kv_write) g_quantized_write;
+decltype(&w4a16_quantized_kv_read) g_quantized_read;
+decltype(&w4a16_quantized_attention) g_quantized_attention;
 
 // What a call's tensors have to share, and whether one of them did not.
 struct Call {
@@ -288,6 +293,168 @@ PyObject *linear_attention_step(PyObject *, PyObject *const *a, Py_ssize_t n)
                          m.ldo, m.hso, c.stream()));
 }
 
+// beta: float32 [T, H] or [H].
+const at::Tensor *rates(Call &c, PyObject *o, const Mixer &m, int64_t *ld, int64_t *hs)
+{
+    if (!THPVariable_Check(o)) {
+        c.ok = false;
+        return nullptr;
+    }
+    const bool each = THPVariable_Unpack(o).dim() == 2;
+    const at::Tensor *t = c.typed(o, each ? 2 : 1, at::kFloat);
+    c.need(c.ok && (each ? t->size(0) == m.T && t->size(1) == m.H : t->size(0) == m.H));
+    if (!c.ok)
+        return nullptr;
+    *ld = each && m.T > 1 ? t->stride(0) : 0;
+    *hs = t->stride(each ? 1 : 0);
+    return t;
+}
+
+// (q, k, v, log_decay, beta, cu_seqlens, state, state_out, scale, out, workspace)
+PyObject *delta_rule(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    Call c;
+    Mixer m;
+    float scale = 0;
+    int64_t ldb = 0, hsb = 0;
+    if (n != 11 || !read_float(a[8], &scale) || !read_mixer(c, a[0], a[1], a[2], a[3], a[9], &m))
+        return status(-1);
+    const at::Tensor *beta = rates(c, a[4], m, &ldb, &hsb), *cu = c.flat(a[5], 1, at::kInt, true);
+    const at::Tensor *s0 = states(c, a[6], m, true), *s1 = states(c, a[7], m, false), *work = c.flat(a[10], 1, at::kByte);
+    if (!c.ready())
+        return status(-1);
+    const int64_t seqs = cu ? cu->size(0) - 1 : 1;
+    c.need(fits(seqs) && s1->size(0) == seqs && (!s0 || s0->size(0) == seqs));
+    if (!c.ok)
+        return status(-1);
+    return status(g_delta(ptr(m.q), m.ldq, m.hsq, ptr(m.k), m.ldk, m.hsk, ptr(m.v), m.ldv, m.hsv, ptr<float>(m.g), m.ldg,
+                          m.hsg, ptr<float>(beta), ldb, hsb, ptr<int32_t>(cu), (int32_t)seqs, (int32_t)m.T, (int32_t)m.Hk,
+                          (int32_t)m.H, (int32_t)m.Dk, (int32_t)m.Dv, type_of(m.q), scale, ptr<float>(s0), ptr<float>(s1),
+                          ptr(m.out), m.ldo, m.hso, ptr(work), work->size(0), c.stream()));
+}
+
+// (q, k, v, log_decay, beta, state, slots, state_out, scale, out)
+PyObject *delta_rule_step(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    Call c;
+    Mixer m;
+    float scale = 0;
+    int64_t ldb = 0, hsb = 0;
+    if (n != 10 || !read_float(a[8], &scale) || !read_mixer(c, a[0], a[1], a[2], a[3], a[9], &m))
+        return status(-1);
+    const at::Tensor *beta = rates(c, a[4], m, &ldb, &hsb), *s0 = states(c, a[5], m, false);
+    const at::Tensor *slots = c.flat(a[6], 1, at::kInt, true), *s1 = states(c, a[7], m, false);
+    if (!c.ready())
+        return status(-1);
+    c.need(fits(s0->size(0)) && s1->size(0) == s0->size(0) && (!slots || slots->size(0) == m.T));
+    if (!c.ok)
+        return status(-1);
+    return status(g_delta_step(ptr(m.q), m.ldq, m.hsq, ptr(m.k), m.ldk, m.hsk, ptr(m.v), m.ldv, m.hsv, ptr<float>(m.g),
+                               m.ldg, m.hsg, ptr<float>(beta), ldb, hsb, ptr<int32_t>(slots), (int32_t)s0->size(0),
+                               (int32_t)m.T, (int32_t)m.Hk, (int32_t)m.H, (int32_t)m.Dk, (int32_t)m.Dv, type_of(m.q), scale,
+                               ptr<float>(s0), ptr<float>(s1), ptr(m.out), m.ldo, m.hso, c.stream()));
+}
+
+// A cache of codes and its scales: (k_cache, v_cache, k_scale, v_scale).
+bool read_quantized(Call &c, PyObject *const *a, w4a16_quantized_cache_t *out)
+{
+    const at::Tensor *k = c.any(a[0], 4), *v = c.any(a[1], 4);
+    const at::Tensor *ks = c.typed(a[2], 3, at::kFloat), *vs = c.typed(a[3], 3, at::kFloat);
+    if (!c.ok || k->scalar_type() != v->scalar_type() || k->sizes() != v->sizes() || ks->sizes() != vs->sizes() ||
+        (k->scalar_type() != at::kChar && k->scalar_type() != at::kFloat8_e4m3fn) || k->stride(3) != 1 || v->stride(3) != 1)
+        return c.ok = false;
+    for (int i = 0; i < 4; ++i)
+        if (!fits(k->size(i)))
+            return c.ok = false;
+    const int64_t blocks = ks->size(1);
+    if (ks->size(0) != k->size(0) || ks->size(2) != k->size(2) || blocks < 1 || k->size(1) % blocks)
+        return c.ok = false;
+    out->k = k->data_ptr();
+    out->v = v->data_ptr();
+    out->k_scale = ptr<float>(ks);
+    out->v_scale = ptr<float>(vs);
+    for (int i = 0; i < 3; ++i) {
+        out->k_stride[i] = k->size(i) > 1 ? k->stride(i) : 0;
+        out->v_stride[i] = v->size(i) > 1 ? v->stride(i) : 0;
+        out->k_scale_stride[i] = ks->stride(i);
+        out->v_scale_stride[i] = vs->stride(i);
+    }
+    out->num_pages = (int32_t)k->size(0);
+    out->page_size = (int32_t)k->size(1);
+    out->heads = (int32_t)k->size(2);
+    out->dim = (int32_t)k->size(3);
+    out->block = (int32_t)(k->size(1) / blocks);
+    out->type = k->scalar_type() == at::kChar ? W4A16_INT8 : W4A16_E4M3;
+    return true;
+}
+
+// k and v rows, a cache (4) and slots, read and checked; false where the call is not taken.
+struct CodeRows {
+    const at::Tensor *k, *v, *slots;
+    int64_t ldk = 0, hsk = 0, ldv = 0, hsv = 0, T = 0;
+    w4a16_quantized_cache_t cache;
+    bool read(PyObject *ko, PyObject *vo, PyObject *const *cache_of, PyObject *so)
+    {
+        Call c;
+        k = c.rows(ko, &ldk, &hsk);
+        v = c.rows(vo, &ldv, &hsv);
+        slots = c.flat(so, 1, at::kInt);
+        if (!c.ok || k->scalar_type() != v->scalar_type() || !read_quantized(c, cache_of, &cache) || !c.ready())
+            return false;
+        T = slots->size(0);
+        stream = c.stream();
+        return fits(T) && k->sizes() == v->sizes() && k->size(0) == T && k->size(1) == cache.heads && k->size(2) == cache.dim;
+    }
+    hipStream_t stream;
+};
+
+// (k, v, k_cache, v_cache, k_scale, v_scale, slot_map)
+PyObject *quantized_kv_write(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    CodeRows r;
+    if (n != 7 || !r.read(a[0], a[1], a + 2, a[6]))
+        return status(-1);
+    return status(g_quantized_write(ptr(r.k), r.ldk, r.hsk, ptr(r.v), r.ldv, r.hsv, (int32_t)r.T, type_of(r.k),
+                                    ptr<int32_t>(r.slots), &r.cache, r.stream));
+}
+
+// (k_cache, v_cache, k_scale, v_scale, slot_map, k, v)
+PyObject *quantized_kv_read(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    CodeRows r;
+    if (n != 7 || !r.read(a[5], a[6], a, a[4]))
+        return status(-1);
+    return status(g_quantized_read(&r.cache, ptr<int32_t>(r.slots), (int32_t)r.T, type_of(r.k), ptr(r.k), r.ldk, r.hsk,
+                                   ptr(r.v), r.ldv, r.hsv, r.stream));
+}
+
+// (q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, scale, window, out, lse, workspace)
+PyObject *quantized_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    Call c;
+    int64_t ldq = 0, hsq = 0, ldo = 0, hso = 0, window = 0;
+    float scale = 0;
+    if (n != 12 || !read_float(a[7], &scale) || !read_int(a[8], &window))
+        return status(-1);
+    const at::Tensor *q = c.rows(a[0], &ldq, &hsq), *table = c.typed(a[5], 2, at::kInt);
+    const at::Tensor *lens = c.flat(a[6], 1, at::kInt), *out = c.rows(a[9], &ldo, &hso);
+    const at::Tensor *lse = c.flat(a[10], 2, at::kFloat, true), *work = c.flat(a[11], 1, at::kByte);
+    w4a16_quantized_cache_t cache;
+    if (!c.ok || !read_quantized(c, a + 1, &cache) || !c.ready())
+        return status(-1);
+    const int64_t B = q->size(0), Hq = q->size(1), pages = table->size(1);
+    c.need(q->size(2) == cache.dim && out->scalar_type() == q->scalar_type() && out->sizes() == q->sizes());
+    c.need(table->size(0) == B && lens->size(0) == B && (pages <= 1 || table->stride(1) == 1));
+    c.need(!lse || (lse->size(0) == B && lse->size(1) == Hq));
+    c.need(fits(B) && fits(Hq) && fits(pages));
+    if (!c.ok)
+        return status(-1);
+    return status(g_quantized_attention(ptr(q), ldq, hsq, type_of(q), &cache, ptr<int32_t>(table),
+                                        B > 1 ? table->stride(0) : pages, (int32_t)pages, ptr<int32_t>(lens), (int32_t)B,
+                                        (int32_t)Hq, scale, (int32_t)window, ptr(out), ldo, hso, ptr<float>(lse), ptr(work),
+                                        work->size(0), c.stream()));
+}
+
 // No C++ exception may leave a function that Python calls.
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
 PyObject *guarded(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -300,22 +467,30 @@ PyObject *guarded(PyObject *self, PyObject *const *a, Py_ssize_t n)
     }
 }
 
-// Addresses of the five C entries, in the order of their declarations.
-PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
+// Five addresses of C entries.
+bool read_addresses(PyObject *const *a, Py_ssize_t n, void **p)
 {
-    void *p[5];
     if (n != 5) {
         PyErr_SetString(PyExc_TypeError, "five addresses are wanted");
-        return nullptr;
+        return false;
     }
     for (int i = 0; i < 5; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i]) {
             if (!PyErr_Occurred())
                 PyErr_SetString(PyExc_ValueError, "null address");
-            return nullptr;
+            return false;
         }
     }
+    return true;
+}
+
+// Page tables, cache writes, attention, and both forms of linear attention.
+PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    void *p[5];
+    if (!read_addresses(a, n, p))
+        return nullptr;
     g_page_tables = (decltype(g_page_tables))p[0];
     g_kv_write = (decltype(g_kv_write))p[1];
     g_attention = (decltype(g_attention))p[2];
@@ -324,10 +499,27 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
     Py_RETURN_NONE;
 }
 
+// Both forms of the delta rule; writes, reads and attention of a cache of codes.
+PyObject *bind_more(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    void *p[5];
+    if (!read_addresses(a, n, p))
+        return nullptr;
+    g_delta = (decltype(g_delta))p[0];
+    g_delta_step = (decltype(g_delta_step))p[1];
+    g_quantized_write = (decltype(g_quantized_write))p[2];
+    g_quantized_read = (decltype(g_quantized_read))p[3];
+    g_quantized_attention = (decltype(g_quantized_attention))p[4];
+    Py_RETURN_NONE;
+}
+
 #define ENTRY(name) {#name, (PyCFunction)(void (*)(void))guarded<name>, METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {ENTRY(page_tables),      ENTRY(paged_kv_write),
                           ENTRY(paged_attention),  ENTRY(linear_attention),
                           ENTRY(linear_attention_step), ENTRY(bind),
+                          ENTRY(delta_rule),       ENTRY(delta_rule_step),
+                          ENTRY(quantized_kv_write), ENTRY(quantized_kv_read),
+                          ENTRY(quantized_attention), ENTRY(bind_more),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods};
 

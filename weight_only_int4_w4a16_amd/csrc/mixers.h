@@ -1,5 +1,5 @@
-// Arguments and launchers of the token mixers: page tables, paged cache writes, paged attention and
-// linear attention. The entry points have checked every argument before a launcher sees it.
+// Arguments and launchers of the token mixers: page tables, paged cache writes, paged attention, linear
+// attention, the gated delta rule, and the cache with a scale for each block of tokens and head. The entry points have checked every argument before a launcher sees it.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -56,15 +56,49 @@ struct LinearArgs {
     float scale;
 };
 
+struct DeltaArgs : LinearArgs {
+    const float *beta;
+    int64_t ldb, hsb;
+};
+
+// A cache of 8-bit codes and its scales (keys, values); strides of scales: page, block, head.
+struct QuantizedCache {
+    uint8_t *codes[2];
+    int64_t page[2], slot[2], head[2];
+    float *scale[2];
+    int64_t scale_page[2], scale_block[2], scale_head[2];
+    int32_t num_pages, page_size, heads, dim, block;
+    int32_t int8;
+};
+
+struct QuantizedRowsArgs {   // rows to or from the slots of a cache
+    QuantizedCache c;
+    void *x[2];
+    int64_t ld[2], hs[2];
+    const int32_t *slot_map;
+    int32_t T, fp16;
+};
+
+struct QuantizedAttentionArgs : AttentionArgs {
+    int64_t k_scale_page, k_scale_block, k_scale_head, v_scale_page, v_scale_block, v_scale_head;
+    int32_t block, int8;
+};
+
 hipError_t launch_page_tables(const PageTablesArgs &a, hipStream_t stream);
 hipError_t launch_kv_write(const KvWriteArgs &a, int cus, hipStream_t stream);
 hipError_t launch_attention(const AttentionArgs &a, int cus, hipStream_t stream);
 hipError_t launch_linear(const LinearArgs &a, hipStream_t stream);
 hipError_t launch_linear_step(const LinearArgs &a, hipStream_t stream);
+hipError_t launch_delta(const DeltaArgs &a, hipStream_t stream);
+hipError_t launch_delta_step(const DeltaArgs &a, hipStream_t stream);
+hipError_t launch_quantized_write(const QuantizedRowsArgs &a, hipStream_t stream);
+hipError_t launch_quantized_read(const QuantizedRowsArgs &a, int cus, hipStream_t stream);
+hipError_t launch_quantized_attention(const QuantizedAttentionArgs &a, int cus, hipStream_t stream);
 
 int64_t attention_workspace(int32_t Hq, int32_t heads, int32_t dim);
 // Most units of work of one request and head.
 int64_t attention_units(int32_t max_pages, int32_t page_size);
 int64_t linear_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk, int32_t Dv);
+int64_t delta_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t type);
 
 }  // namespace w4a16

@@ -62,6 +62,8 @@ def _library():
         _binding = binding
         _binding.bind(*[ctypes.cast(getattr(lib, "w4a16_" + n), _P).value for n in (
             "page_tables", "paged_kv_write", "paged_attention", "linear_attention", "linear_attention_step")])
+        _binding.bind_more(*[ctypes.cast(getattr(lib, "w4a16_" + n), _P).value for n in (
+            "delta_rule", "delta_rule_step", "quantized_kv_write", "quantized_kv_read", "quantized_attention")])
         row = [_P, _i64, _i64]
         lib.w4a16_page_tables.argtypes = [_P, _P, _i32, _P, _i64, _i32, _P, _i32, _i32, _i32,
                                           _P, _P, _P, _P, _P, _P]
@@ -75,8 +77,19 @@ def _library():
         lib.w4a16_linear_attention_workspace.argtypes = [_i32] * 5
         lib.w4a16_linear_attention_workspace.restype = _i64
         lib.w4a16_linear_attention_step.argtypes = row * 4 + [_P] + [_i32] * 7 + [_f32, _P, _P] + row + [_P]
+        lib.w4a16_delta_rule.argtypes = row * 5 + [_P] + [_i32] * 7 + [_f32, _P, _P] + row + [_P, _i64, _P]
+        lib.w4a16_delta_rule_workspace.argtypes = [_i32] * 6
+        lib.w4a16_delta_rule_workspace.restype = _i64
+        lib.w4a16_delta_rule_step.argtypes = row * 5 + [_P] + [_i32] * 7 + [_f32, _P, _P] + row + [_P]
+        lib.w4a16_quantized_kv_write.argtypes = row + row + [_i32, _i32, _P, _P, _P]
+        lib.w4a16_quantized_kv_read.argtypes = [_P, _P, _i32, _i32] + row + row + [_P]
+        lib.w4a16_quantized_attention.argtypes = lib.w4a16_paged_attention.argtypes
+        lib.w4a16_quantized_attention_workspace.argtypes = [_i32, _i32, _i32]
+        lib.w4a16_quantized_attention_workspace.restype = _i64
         for f in (lib.w4a16_page_tables, lib.w4a16_paged_kv_write, lib.w4a16_paged_attention,
-                  lib.w4a16_linear_attention, lib.w4a16_linear_attention_step):
+                  lib.w4a16_linear_attention, lib.w4a16_linear_attention_step, lib.w4a16_delta_rule,
+                  lib.w4a16_delta_rule_step, lib.w4a16_quantized_kv_write, lib.w4a16_quantized_kv_read,
+                  lib.w4a16_quantized_attention):
             f.restype = ctypes.c_int
         _lib = lib
     return _lib
