@@ -212,6 +212,56 @@ __device__ __forceinline__ void store_out(const AttentionArgs &a, int64_t b, int
     *(u32x2 *)((uint16_t *)a.out + b * a.ldo + h * a.hso + d) = r;
 }
 
+// ---- one tile's operands -------------------------------------------------------------------------
+
+// Words of 16-bit values per lane and V row; a row is loaded in parts of 16 lanes each:
+// 64 dims (4 per lane), 96 (4 and 2), 128 (8), 192 (8 and 4), 256 (8 and 8).
+template <int D>
+struct Parts {
+    static constexpr int words = D / 32;
+    static constexpr int first = D >= 128 ? 8 : 4;            // dims per lane of the first part
+    static constexpr int second = D / 16 - first;             // and of the second, or 0
+    // dim of local value j of lane i
+    static __device__ __forceinline__ int dim(int i, int j)
+    {
+        return j < first ? first * i + j : 16 * first + second * i + (j - first);
+    }
+};
+
+// N 16-bit values (N / 2 words) from memory, or N e4m3 codes (N / 4 words, at least one).
+template <int N, bool E4M3>
+__device__ __forceinline__ void load_part(const uint8_t *p, uint32_t *r)
+{
+    constexpr int bytes = E4M3 ? N : 2 * N;
+    if constexpr (bytes == 16) {
+        const u32x4 x = __builtin_nontemporal_load((const u32x4 *)p);
+        r[0] = x[0]; r[1] = x[1]; r[2] = x[2]; r[3] = x[3];
+    } else if constexpr (bytes == 8) {
+        const u32x2 x = __builtin_nontemporal_load((const u32x2 *)p);
+        r[0] = x[0]; r[1] = x[1];
+    } else if constexpr (bytes == 4) {
+        r[0] = *(const uint32_t *)p;
+    } else {
+        static_assert(bytes == 2, "parts are 2 to 16 bytes");
+        r[0] = *(const uint16_t *)p;
+    }
+}
+
+// K rows as the first operand of S^T = K Q^T: lane % 16 is the position, and a contraction of 32 dims
+// takes 8 from each of the four lanes of a position. bfloat16 / float16: dims 32c + 8g. e4m3: one
+// 16-byte load serves two contractions (dims 64 (c / 2) + 16 g + 8 (c % 2)), the last 32 of 96
+// dims come in 8-byte loads.
+template <int D, bool E4M3>
+struct KeyDims {
+    static constexpr int chunks = D / 32, paired = E4M3 ? D / 64 * 2 : 0;
+    static __device__ __forceinline__ int dim(int c, int g)
+    {
+        return c < paired ? 64 * (c / 2) + 16 * g + 8 * (c % 2) : 32 * c + 8 * g;
+    }
+};
+
+// ---- the second launch ---------------------------------------------------------------------------
+
 // Joins the pieces of a (request, head) that several work-groups share; the one that holds its end
 // has left a note. A thread sums four dims of one head over every `parts`-th piece, with the maximum
 // running along; the parts are then joined in order. (With the notes instead of another search for
