@@ -168,8 +168,8 @@ __device__ __forceinline__ int32_t first_place(const DeltaArgs &a, int s)
 }
 __device__ __forceinline__ void tokens_of(const DeltaArgs &a, int s, int32_t *t0, int32_t *t1)
 {
-    *t0 = a.cu ? min(max(a.cu[s], 0), a.T) : 0;
-    *t1 = a.cu ? max(min(max(a.cu[s + 1], 0), a.T), *t0) : a.T;
+    *t0 = a.cu ? __builtin_amdgcn_readfirstlane(min(max(a.cu[s], 0), a.T)) : 0;
+    *t1 = a.cu ? max(__builtin_amdgcn_readfirstlane(min(max(a.cu[s + 1], 0), a.T)), *t0) : a.T;
 }
 
 // The last sequence whose places start at or before `place`, or -1; 64 of them at a time.
@@ -405,19 +405,6 @@ __device__ __forceinline__ f32x4 mfma_words(u32x2 a, u32x2 b, f32x4 c)
 }
 __device__ __forceinline__ f32x4 mfma_words(u32x4 a, u32x4 b, f32x4 c) { return mfma(Bf16(), a, b, c); }
 
-// N + M terms of two operands' products that are above 2^-24 of the whole, the small ones first.
-template <int NA, int NB, int MOST, class V>
-__device__ __forceinline__ f32x4 products(const V *x, const V *y, f32x4 c)
-{
-#pragma unroll
-    for (int sum = MOST; sum >= 0; --sum)
-#pragma unroll
-        for (int i = 0; i < NA; ++i)
-            if (sum - i >= 0 && sum - i < NB)
-                c = mfma_words(x[i], y[sum - i], c);
-    return c;
-}
-
 template <int N>
 struct WordsOf;
 template <>
@@ -431,71 +418,68 @@ struct WordsOf<4> {
     static __device__ __forceinline__ T load(Rows r, uint32_t at) { return load4(r, at); }
 };
 
-// A work-group goes over the chunks of one sequence, head and 16 columns. Wave w holds the rows of S with dk in
-// [DK / 4 w, DK / 4 (w + 1)), in float32, and multiplies K and Q by them as they are: a lane's values of S are the
-// second operand's, for the same dims of a K row. The four waves' sums of X meet in LDS, wave w takes the tokens
-// 16 w .. on to R; R and U are shared through LDS in operand order, so that no other values cross lanes.
-template <class Type, int DK>
-__global__ __launch_bounds__(kDeltaThreads, 2) void delta_chunk_kernel(DeltaArgs a, const Prepared<Type> *work, int slices)
+// The products of NA and NB terms of two operands that matter (of term i and j with i + j <= MOST), small ones
+// first, for N results side by side: none waits for the one before it.
+template <int NA, int NB, int MOST, int N, class A, class B>
+__device__ __forceinline__ void products(const A &a, const B &b, f32x4 *c)
+{
+#pragma unroll
+    for (int sum = MOST; sum >= 0; --sum)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (sum - i >= 0 && sum - i < NB)
+#pragma unroll
+                for (int x = 0; x < N; ++x)
+                    c[x] = mfma_words(a(x, i), b(x, sum - i), c[x]);
+}
+
+// What a work-group's waves share. Operands that go from wave to wave lie as the reader's lanes need them.
+template <class Words>
+struct DeltaLds {
+    f32x4 x[kWaves][kWaves][64];                      // K S: sums over a wave's rows of S, for each tile of tokens
+    Words s[2][kWaves][64];                           // S, two terms
+    u32x2 r[3][2][64][2], u[3][2][64][2], uo[2][2][64][2];   // R, e^(b_63 - b) U, U
+    f32x4 v[kWaves][64];                              // V: tokens 16 w + 4 g .. of a column
+    Words k[kWaves][kChunk][5];                       // a wave's part of K, rows 4 words or 2 and a pad of as many
+    int32_t bad[2][16], odd[2];                       // values that are not finite: first tokens by column, whether any
+};
+
+struct DeltaUnit {
+    int32_t t0, t1, hk, h, c0;
+    int64_t unit;
+};
+
+// Waves 0 to 3 carry the state: wave w holds the rows of S with dk in [DK / 4 w, DK / 4 (w + 1)), in float32, and
+// multiplies K by them as they are: a lane's values of S are the second operand's, for the same dims of a K row. The
+// four sums of X meet in LDS; wave w takes the tokens 16 w .. on to R and U, which all need.
+template <class Type, int DK, class Lds>
+__device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<Type> *from, const DeltaUnit &d, int w, Lds &lds)
 {
     constexpr int EK = DK / 64, NW = 2 * EK, KT = Split<Type>::terms, PT = Prepared<Type>::p_terms;
     typedef typename WordsOf<NW>::T Words;
-    __shared__ f32x4 lds_x[kWaves][kWaves][64], lds_q[kWaves][kWaves][64];
-    __shared__ __align__(16) u32x2 lds_r[3][2][64][2], lds_u[5][2][64][2];
-    __shared__ int32_t lds_bad[2][16], lds_odd[2];
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int col = lane & 15, g = lane >> 4;
-    // All slices of a head on one XCD (work-groups go to the 8 of them in turn).
-    const int64_t rest = blockIdx.x / 8, unit = rest / slices * 8 + blockIdx.x % 8;
-    if (unit >= (int64_t)a.B * a.H)
-        return;
-    const int seq = (int)(unit / a.H), h = (int)(unit - (int64_t)seq * a.H), hk = h / (a.H / a.Hk);
-    const int c0 = (int)(rest % slices) * 16;
-    int32_t t0, t1;
-    tokens_of(a, seq, &t0, &t1);
-    const Prepared<Type> *from = work + (int64_t)first_place(a, seq) * a.H + h;
-    const uint16_t *qp = (const uint16_t *)a.q + hk * a.hsq, *kp = (const uint16_t *)a.k + hk * a.hsk;
-    const uint16_t *vp = (const uint16_t *)a.v + h * a.hsv + c0;
-    uint16_t *op = (uint16_t *)a.out + h * a.hso + c0;
-    const int32_t ldq = (int32_t)a.ldq, ldk = (int32_t)a.ldk, ldv = (int32_t)a.ldv, ldo = (int32_t)a.ldo;
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    const int32_t t0 = d.t0, t1 = d.t1;
+    const uint16_t *kp = (const uint16_t *)a.k + d.hk * a.hsk;
+    const int32_t ldk = (int32_t)a.ldk;
 
     // s[j][r]: row DK / 4 w + EK (4 g + r) + j
-    const int64_t state_at = ((int64_t)unit * DK + DK / 4 * w + EK * 4 * g) * a.Dv + c0 + col;
+    const int64_t state_at = (d.unit * DK + DK / 4 * w + EK * 4 * g) * a.Dv + d.c0 + col;
     f32x4 s[EK];
 #pragma unroll
     for (int j = 0; j < EK; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             s[j][r] = a.state_in ? a.state_in[state_at + (int64_t)(EK * r + j) * a.Dv] : 0.0f;
-    if (tid < 32)
-        lds_bad[tid >> 4][tid & 15] = kChunk;
-    if (tid < 2)
-        lds_odd[tid] = 0;
 
-    Words kn[kWaves], qn[kWaves];   // rows 16 i + col, this wave's dims from 4 EK g on
-    uint32_t kt[16];                // dims EK col .. of tokens 32 c + 16 x + 4 g + e
-    u32x4 tn[3][2], pn[PT][2];
-    uint32_t vn[4];                 // tokens 16 w + 4 g ..
+    Words kn[kWaves];        // rows 16 i + col, this wave's dims from 4 EK g on
+    u32x4 tn[3][2];
     f32x4 ebn, edn;
-    int32_t badn = kChunk;
-    float wholen = 1.0f;
-    auto fetch_kq = [&](int32_t t) {
+    u32x2 endn = {kChunk, 0};
+    auto fetch_k = [&](int32_t t) {
         const Rows kr = rows_of(kp + (int64_t)t * ldk, t1 - t, ldk, DK, 2);
-        const Rows qr = rows_of(qp + (int64_t)t * ldq, t1 - t, ldq, DK, 2);
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) {
+        for (int i = 0; i < kWaves; ++i)
             kn[i] = WordsOf<NW>::load(kr, 2 * ((16 * i + col) * (uint32_t)ldk + DK / 4 * w + 4 * EK * g));
-            qn[i] = WordsOf<NW>::load(qr, 2 * ((16 * i + col) * (uint32_t)ldq + DK / 4 * w + 4 * EK * g));
-        }
-    };
-    auto fetch_kt = [&](int32_t t) {
-        const Rows kr = rows_of(kp + (int64_t)t * ldk, t1 - t, ldk, DK, 2);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const uint32_t at = 2 * ((32 * (e / 8) + 16 * (e / 4 % 2) + 4 * g + e % 4) * (uint32_t)ldk + DK / 4 * w + EK * col);
-            kt[e] = EK == 2 ? __builtin_amdgcn_raw_buffer_load_b32(kr, at, 0, 0)
-                            : __builtin_amdgcn_raw_buffer_load_b16(kr, at, 0, 0);
-        }
     };
     auto prepared = [&](int32_t t) {   // zeros past the last chunk; operands that are none lie past its end
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>((const void *)from), 0,
@@ -508,42 +492,32 @@ __global__ __launch_bounds__(kDeltaThreads, 2) void delta_chunk_kernel(DeltaArgs
             for (int c = 0; c < 2; ++c)
                 tn[i][c] = load4(x, c <= w / 2 ? (uint32_t)((i * kFrags + frag(w, c)) * 64 + lane) * 16 : ~0u);
     };
-    auto fetch_p = [&](Rows x) {
-#pragma unroll
-        for (int i = 0; i < PT; ++i)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                pn[i][c] = load4(x, c <= w / 2 ? (uint32_t)(((3 + i) * kFrags + frag(w, c)) * 64 + lane) * 16 : ~0u);
-    };
-    auto fetch_v = [&](int32_t t, Rows x) {
-        const Rows vr = rows_of(vp + (int64_t)t * ldv, t1 - t, ldv, 16, 2);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            vn[r] = __builtin_amdgcn_raw_buffer_load_b16(vr, 2 * ((16 * w + 4 * g + r) * (uint32_t)ldv + col), 0, 0);
+    auto fetch_factors = [&](Rows x) {
         constexpr uint32_t at = (3 + PT) * kFrags * 64 * 16;
         ebn = __builtin_bit_cast(f32x4, load4(x, at + 4 * (16 * w + 4 * g)));
         edn = __builtin_bit_cast(f32x4, load4(x, at + 4 * (kChunk + 16 * w + 4 * g)));
-        badn = __builtin_amdgcn_raw_buffer_load_b32(x, at + 8 * kChunk, 0, 0);
-        wholen = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(x, at + 8 * kChunk + 4, 0, 0));
+        endn = __builtin_amdgcn_raw_buffer_load_b64(x, at + 8 * kChunk, 0, 0);
     };
     if (t0 < t1) {
         const Rows x = prepared(t0);
-        fetch_kq(t0);
-        fetch_v(t0, x);
+        fetch_k(t0);
+        fetch_factors(x);
         fetch_t(x);
-        fetch_kt(t0);
-        fetch_p(x);
     }
-    __syncthreads();
+    // The loop would wait for them, and then in every round for all that is in flight.
+#pragma unroll
+    for (int j = 0; j < EK; ++j)
+        asm volatile("" : "+v"(s[j]));
 
     int parity = 0;
     for (int32_t t = t0; t < t1; t += kChunk, parity ^= 1) {
         const int32_t n = min(t1 - t, kChunk);
         from += a.H;
         const Rows next = prepared(t + kChunk);
-        // X and Q S: this wave's dims
+        // X: this wave's dims
+        Words sb[3], k[kWaves];
         {
-            Words sb[3];
+            Words ka[kWaves][KT];
 #pragma unroll
             for (int i = 0; i < NW; ++i) {
                 float x = EK == 2 ? s[0][i] : s[0][2 * i], y = EK == 2 ? s[EK - 1][i] : s[0][2 * i + 1];
@@ -551,167 +525,152 @@ __global__ __launch_bounds__(kDeltaThreads, 2) void delta_chunk_kernel(DeltaArgs
                 for (int term = 0; term < 3; ++term)
                     sb[term][i] = take(Bf16(), x, y);
             }
+            f32x4 x[kWaves];
 #pragma unroll
             for (int i = 0; i < kWaves; ++i) {
-                Words ka[KT], qa[KT];
+                x[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                k[i] = kn[i];
 #pragma unroll
                 for (int j = 0; j < NW; ++j) {
                     uint32_t o[KT];
-                    Split<Type>::of(kn[i][j], o);
+                    Split<Type>::of(k[i][j], o);
 #pragma unroll
                     for (int term = 0; term < KT; ++term)
-                        ka[term][j] = o[term];
-                    Split<Type>::of(qn[i][j], o);
-#pragma unroll
-                    for (int term = 0; term < KT; ++term)
-                        qa[term][j] = o[term];
+                        ka[i][term][j] = o[term];
                 }
-                const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-                lds_x[w][i][lane] = products<KT, 3, 2>(ka, sb, zero);
-                lds_q[w][i][lane] = products<KT, 2, 1>(qa, sb, zero);
             }
+            lds.s[0][w][lane] = sb[0];
+            lds.s[1][w][lane] = sb[1];
+            products<KT, 3, 2, kWaves>([&](int i, int term) { return ka[i][term]; },
+                                       [&](int, int term) { return sb[term]; }, x);
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i)
+                lds.x[w][i][lane] = x[i];
         }
-        fetch_kq(t + kChunk);
+        fetch_k(t + kChunk);
         __syncthreads();
 
-        // R and e^b Q S of tokens 16 w ..
+        // R of tokens 16 w ..
         const f32x4 eb = ebn, ed = edn;
-        const int32_t bad = __builtin_amdgcn_readfirstlane(badn), lim = min(n, bad);
-        const float whole = wholen;
-        f32x4 x = lds_x[0][w][lane], o = lds_q[0][w][lane];
+        const int32_t bad = __builtin_amdgcn_readfirstlane(endn[0]), lim = min(n, bad);
+        const uint32_t whole_bits = endn[1];
+        const float whole = __builtin_bit_cast(float, whole_bits);
+        f32x4 xs[kWaves];
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) {
-            const f32x4 y = lds_x[i][w][lane], z = lds_q[i][w][lane];
+        for (int i = 0; i < kWaves; ++i)
+            xs[i] = lds.x[i][w][lane];
+        const f32x4 v = lds.v[w][lane];
+        // While these come: K, for a look at it from the other side.
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                x[r] += y[r];
-                o[r] += z[r];
-            }
+        for (int i = 0; i < kWaves; ++i)
+            lds.k[w][16 * i + col][g] = k[i];
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4 x;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            x[r] = fmaf(-eb[r], (xs[0][r] + xs[1][r]) + (xs[2][r] + xs[3][r]), v[r]);
+        if (lim < kChunk) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                x[r] = 16 * w + 4 * g + r < lim ? x[r] : 0.0f;
         }
-        float v[4], check = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            v[r] = low(Type(), vn[r]);
-            check = fmaf(v[r], 0.0f, check);
-        }
-        if (__ballot(check != check)) {   // values that are not finite: zeros, and a mark for what comes after them
-            rare();
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int32_t token = 16 * w + 4 * g + r;
-                if (!(fabsf(v[r]) < INFINITY)) {
-                    v[r] = 0.0f;
-                    if (token < n)
-                        atomicMin(&lds_bad[parity][col], token);
-                }
-            }
-            lds_odd[parity] = 1;
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            x[r] = 16 * w + 4 * g + r < lim ? fmaf(-eb[r], x[r], v[r]) : 0.0f;
-            o[r] *= eb[r];
-        }
-        fetch_v(t + kChunk, next);
 #pragma unroll
         for (int term = 0; term < 3; ++term)
-            lds_r[term][w / 2][lane][w & 1] = take4(x);
+            lds.r[term][w / 2][lane][w & 1] = take4(x);
+        fetch_factors(next);
         __syncthreads();
 
         // U of tokens 16 w ..
-        const bool odd = __builtin_amdgcn_readfirstlane(lds_odd[parity]) != 0;
-        f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            u32x4 ta[3], rb[3];
-#pragma unroll
-            for (int term = 0; term < 3; ++term) {
-                ta[term] = tn[term][c];
-                rb[term] = *(const u32x4 *)lds_r[term][c][lane];
-            }
-            u = products<3, 3, 2>(ta, rb, u);
-        }
-        fetch_t(next);
+        const bool odd = __builtin_amdgcn_readfirstlane(lds.odd[parity]) != 0;
+        f32x4 u[2];
         {
-            f32x4 y = u, z;
+            u32x4 rb[2][3];
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                z[r] = u[r] * ed[r];
+            for (int c = 0; c < 2; ++c) {
+                u[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int term = 0; term < 3; ++term) {
-                lds_u[term][w / 2][lane][w & 1] = take4(z);
-                if (term < 2)
-                    lds_u[3 + term][w / 2][lane][w & 1] = take4(y);
+                for (int term = 0; term < 3; ++term)
+                    rb[c][term] = *(const u32x4 *)lds.r[term][c][lane];
             }
+            products<3, 3, 2, 2>([&](int c, int term) { return tn[term][c]; },
+                                 [&](int c, int term) { return rb[c][term]; }, u);
         }
-        if (w == 0 && lane < 16) {   // the last chunk's marks have been read
-            lds_bad[parity ^ 1][lane] = kChunk;
-            if (lane == 0)
-                lds_odd[parity ^ 1] = 0;
-        }
-        __syncthreads();
-
-        // S, and the outputs of tokens 16 w ..
+        {
+            f32x4 y, z;
 #pragma unroll
-        for (int j = 0; j < EK; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                s[j][r] *= whole;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            u32x4 ub[3], ka[EK][KT];
+            for (int r = 0; r < 4; ++r) {
+                y[r] = u[0][r] + u[1][r];
+                z[r] = y[r] * ed[r];
+            }
 #pragma unroll
             for (int term = 0; term < 3; ++term)
-                ub[term] = *(const u32x4 *)lds_u[term][c][lane];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < EK; ++j) {
-                    uint32_t d[KT];
-                    Split<Type>::of(__builtin_amdgcn_perm(kt[8 * c + 2 * i + 1], kt[8 * c + 2 * i],
-                                                          j ? 0x07060302u : 0x05040100u), d);
-#pragma unroll
-                    for (int term = 0; term < KT; ++term)
-                        ka[j][term][i] = d[term];
-                }
-#pragma unroll
-            for (int j = 0; j < EK; ++j)
-                s[j] = products<KT, 3, 2>(ka[j], ub, s[j]);
-        }
-        fetch_kt(t + kChunk);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            u32x4 ub[2], pa[PT];
+                lds.u[term][w / 2][lane][w & 1] = take4(z);
 #pragma unroll
             for (int term = 0; term < 2; ++term)
-                ub[term] = *(const u32x4 *)lds_u[3 + term][c][lane];
-#pragma unroll
-            for (int term = 0; term < PT; ++term)
-                pa[term] = pn[term][c];
-            o = products<PT, 2, 1>(pa, ub, o);
+                lds.uo[term][w / 2][lane][w & 1] = take4(y);
         }
-        fetch_p(next);
-        int32_t reached = bad;
-        if (odd) {
-            rare();
-            reached = min(reached, lds_bad[parity][col]);
+        if (w == 0 && lane < 16) {   // the last chunk's marks have been read
+            lds.bad[parity ^ 1][lane] = kChunk;
+            if (lane == 0)
+                lds.odd[parity ^ 1] = 0;
+        }
+        u32x4 ka[2][EK][KT];   // K with tokens in pairs: dims EK col .. of tokens 32 c + 16 x + 4 g + e
+        {
+            uint32_t kt[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const uint16_t *p = (const uint16_t *)lds.k[w][32 * (e / 8) + 16 * (e / 4 % 2) + 4 * g + e % 4] + EK * col;
+                kt[e] = EK == 2 ? *(const uint32_t *)p : *p;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < EK; ++j) {
+                        uint32_t o[KT];
+                        Split<Type>::of(__builtin_amdgcn_perm(kt[8 * c + 2 * i + 1], kt[8 * c + 2 * i],
+                                                              j ? 0x07060302u : 0x05040100u), o);
+#pragma unroll
+                        for (int term = 0; term < KT; ++term)
+                            ka[c][j][term][i] = o[term];
+                    }
+        }
+        fetch_t(next);
+        __syncthreads();
+
+        // S
+        {
+            u32x4 ub[2][3];
+            f32x4 sum[2 * EK];   // of each half of the chunk
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int term = 0; term < 3; ++term)
+                    ub[c][term] = *(const u32x4 *)lds.u[term][c][lane];
+#pragma unroll
+            for (int j = 0; j < EK; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    sum[j][r] = s[j][r] * whole;
+                    sum[EK + j][r] = 0.0f;
+                }
+            products<KT, 3, 2, 2 * EK>([&](int x, int term) { return ka[x / EK][x % EK][term]; },
+                                       [&](int x, int term) { return ub[x / EK][term]; }, sum);
+#pragma unroll
+            for (int j = 0; j < EK; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    s[j][r] = sum[j][r] + sum[EK + j][r];
         }
         if (odd || bad < n) {
             rare();
+            const int32_t reached = min(bad, lds.bad[parity][col]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                o[r] = 16 * w + 4 * g + r >= reached ? NAN : o[r];
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int j = 0; j < EK; ++j)
                     s[j][r] = reached < n ? NAN : s[j][r];
-            }
-        }
-        const Rows rows = rows_of(op + (int64_t)t * ldo, n, ldo, 16, 2);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int32_t token = 16 * w + 4 * g + r;
-            const uint32_t y = pack2(Type(), o[r] * a.scale, 0.0f);
-            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)y, rows, token < n ? 2 * (token * (uint32_t)ldo + col) : ~0u, 0, 0);
         }
     }
 #pragma unroll
@@ -719,6 +678,173 @@ __global__ __launch_bounds__(kDeltaThreads, 2) void delta_chunk_kernel(DeltaArgs
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             a.state_out[state_at + (int64_t)(EK * r + j) * a.Dv] = s[j][r];
+}
+
+// Waves 4 to 7 make the outputs, next to the others on their SIMDs: wave 4 + w those of the tokens 16 w .., transposed,
+// so that a lane has four columns of one token. They also bring V to the others, as float32.
+template <class Type, int DK, class Lds>
+__device__ __forceinline__ void make_outputs(const DeltaArgs &a, const Prepared<Type> *from, const DeltaUnit &d, int w, Lds &lds)
+{
+    constexpr int EK = DK / 64, NW = 2 * EK, KT = Split<Type>::terms, PT = Prepared<Type>::p_terms;
+    typedef typename WordsOf<NW>::T Words;
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4, token = 16 * w + col;
+    const int32_t t0 = d.t0, t1 = d.t1;
+    const uint16_t *qp = (const uint16_t *)a.q + d.hk * a.hsq, *vp = (const uint16_t *)a.v + d.h * a.hsv + d.c0;
+    uint16_t *op = (uint16_t *)a.out + d.h * a.hso + d.c0;
+    const int32_t ldq = (int32_t)a.ldq, ldv = (int32_t)a.ldv, ldo = (int32_t)a.ldo;
+    Words qn[kWaves];   // dims of wave i from 4 EK g on
+    u32x4 pn[PT][2];
+    u32x2 vn;           // columns 4 g ..
+    float ebn = 0.0f;
+    int32_t badn = kChunk;
+    constexpr uint32_t at = (3 + PT) * kFrags * 64 * 16;
+    auto prepared = [&](int32_t t) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>((const void *)from), 0,
+                                                 t < t1 ? sizeof(Prepared<Type>) : 0, 0x00027000);
+    };
+    auto fetch_v = [&](int32_t t) {
+        vn = WordsOf<2>::load(rows_of(vp + (int64_t)t * ldv, t1 - t, ldv, 16, 2), 2 * (token * (uint32_t)ldv + 4 * g));
+    };
+    auto fetch_q = [&](int32_t t, Rows x) {
+        const Rows qr = rows_of(qp + (int64_t)t * ldq, t1 - t, ldq, DK, 2);
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i)
+            qn[i] = WordsOf<NW>::load(qr, 2 * (token * (uint32_t)ldq + DK / 4 * i + 4 * EK * g));
+        ebn = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(x, at + 4 * token, 0, 0));
+        badn = __builtin_amdgcn_raw_buffer_load_b32(x, at + 8 * kChunk, 0, 0);
+    };
+    auto fetch_p = [&](Rows x) {
+#pragma unroll
+        for (int i = 0; i < PT; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                pn[i][c] = load4(x, c <= w / 2 ? (uint32_t)(((3 + i) * kFrags + frag(w, c)) * 64 + lane) * 16 : ~0u);
+    };
+    if (t0 < t1) {
+        const Rows x = prepared(t0);
+        fetch_v(t0);
+        fetch_q(t0, x);
+        fetch_p(x);
+    }
+    int parity = 0;
+    for (int32_t t = t0; t < t1; t += kChunk, parity ^= 1) {
+        const int32_t n = min(t1 - t, kChunk);
+        from += a.H;
+        const Rows next = prepared(t + kChunk);
+        float v[4] = {low(Type(), vn[0]), high(Type(), vn[0]), low(Type(), vn[1]), high(Type(), vn[1])}, check = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            check = fmaf(v[r], 0.0f, check);
+        if (__ballot(check != check)) {   // values that are not finite: zeros, and a mark for what comes after them
+            rare();
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (!(fabsf(v[r]) < INFINITY)) {
+                    v[r] = 0.0f;
+                    if (token < n)
+                        atomicMin(&lds.bad[parity][4 * g + r], token);
+                }
+            lds.odd[parity] = 1;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            lds.v[w][16 * (col / 4) + 4 * g + r][col % 4] = v[r];
+        fetch_v(t + kChunk);
+        Words qa[kWaves][KT];
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i)
+#pragma unroll
+            for (int j = 0; j < NW; ++j) {
+                uint32_t x[KT];
+                Split<Type>::of(qn[i][j], x);
+#pragma unroll
+                for (int term = 0; term < KT; ++term)
+                    qa[i][term][j] = x[term];
+            }
+        const float eb = ebn;
+        const int32_t bad = __builtin_amdgcn_readfirstlane(badn);
+        __syncthreads();
+
+        f32x4 o[kWaves];   // Q S, over the rows of each wave
+        {
+            Words sb[kWaves][2];
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                sb[i][0] = lds.s[0][i][lane];
+                sb[i][1] = lds.s[1][i][lane];
+            }
+            products<2, KT, 1, kWaves>([&](int i, int term) { return sb[i][term]; },
+                                       [&](int i, int term) { return qa[i][term]; }, o);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                o[0][r] = eb * ((o[0][r] + o[1][r]) + (o[2][r] + o[3][r]));
+                o[1][r] = 0.0f;
+            }
+        }
+        fetch_q(t + kChunk, next);
+        __syncthreads();
+        __syncthreads();
+
+        const bool odd = __builtin_amdgcn_readfirstlane(lds.odd[parity]) != 0;
+        {
+            u32x4 ub[2][2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int term = 0; term < 2; ++term)
+                    ub[c][term] = *(const u32x4 *)lds.uo[term][c][lane];
+            products<2, PT, 1, 2>([&](int c, int term) { return ub[c][term]; },
+                                  [&](int c, int term) { return pn[term][c]; }, o);
+        }
+        fetch_p(next);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            o[0][r] = (o[0][r] + o[1][r]) * a.scale;
+        if (odd || bad < n) {
+            rare();
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                o[0][r] = token >= min(bad, lds.bad[parity][4 * g + r]) ? NAN : o[0][r];
+        }
+        const u32x2 y = {pack2(Type(), o[0][0], o[0][1]), pack2(Type(), o[0][2], o[0][3])};
+        __builtin_amdgcn_raw_buffer_store_b64(y, rows_of(op + (int64_t)t * ldo, n, ldo, 16, 2),
+                                              token < n ? 2 * (token * (uint32_t)ldo + 4 * g) : ~0u, 0, 0);
+    }
+}
+
+// A work-group goes over the chunks of one sequence, head and 16 columns.
+constexpr int kChunkThreads = 512;
+
+template <class Type, int DK>
+__global__ __launch_bounds__(kChunkThreads, 2) void delta_chunk_kernel(DeltaArgs a, const Prepared<Type> *work, int slices)
+{
+    typedef typename WordsOf<DK / 32>::T Words;
+    __shared__ __align__(16) DeltaLds<Words> lds;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // All slices of a head on one XCD (work-groups go to the 8 of them in turn).
+    const uint32_t rest = blockIdx.x / 8, unit = rest / (uint32_t)slices * 8 + blockIdx.x % 8;
+    if (unit >= (uint32_t)a.B * (uint32_t)a.H)   // 2^26 at most
+        return;
+    const int seq = (int)(unit / (uint32_t)a.H);
+    DeltaUnit d;
+    d.unit = unit;
+    d.h = (int)(unit - (uint32_t)seq * (uint32_t)a.H);
+    d.hk = d.h / (a.H / a.Hk);
+    d.c0 = (int)(rest % slices) * 16;
+    tokens_of(a, seq, &d.t0, &d.t1);
+    const Prepared<Type> *from = work + (int64_t)__builtin_amdgcn_readfirstlane(first_place(a, seq)) * a.H + d.h;
+    if (tid < 32)
+        lds.bad[tid >> 4][tid & 15] = kChunk;
+    if (tid < 2)
+        lds.odd[tid] = 0;
+    __syncthreads();
+    if (wave < kWaves) {
+        __builtin_amdgcn_s_setprio(3);   // the others have time
+        carry_state<Type, DK>(a, from, d, wave, lds);
+    } else {
+        make_outputs<Type, DK>(a, from, d, wave - kWaves, lds);
+    }
 }
 
 int64_t places(int32_t T, int32_t num_seqs) { return num_seqs == 1 ? ((int64_t)T + kChunk - 1) / kChunk : T / kChunk + (int64_t)num_seqs; }
@@ -732,7 +858,7 @@ hipError_t delta_of(const DeltaArgs &a, hipStream_t stream)
     const int64_t units = ((int64_t)a.B * a.H + 7) / 8 * 8;
     if (a.T > 0)
         delta_prepare_kernel<Type, DK><<<dim3((unsigned)places(a.T, a.B), a.H), block, 0, stream>>>(a, work);
-    delta_chunk_kernel<Type, DK><<<dim3((unsigned)(units * slices)), block, 0, stream>>>(a, work, slices);
+    delta_chunk_kernel<Type, DK><<<dim3((unsigned)(units * slices)), dim3(kChunkThreads), 0, stream>>>(a, work, slices);
     return hipGetLastError();
 }
 
