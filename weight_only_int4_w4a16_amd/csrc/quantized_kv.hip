@@ -6,8 +6,8 @@
 //
 // Roundings go by the exact quotients and products. Scales come from the values, so quotients on a border
 // between two codes are common (one in a thousand, where 8-bit significands divide), and a float32 quotient
-// falls on the border from both sides. A float32 result next to the exact one, with the sign of what it is off by (one
-// fused operation, exact), is made odd where it is not exact: it then rounds to fewer bits as the exact one.
+// falls on the border from both sides. Of the two float32 values around the exact one the odd one is taken: it rounds
+// to fewer bits as the exact one does. Which it is shows the sign of what is missing, from one fused operation.
 #include "mixers.h"
 #include "mixer_types.h"
 
@@ -15,23 +15,22 @@ namespace w4a16 {
 
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256, kRowWaves = kRowThreads / 64;
 constexpr float kLeast = 0x1p-126f;
 
-// x, one of the two float32 values around a real one (or it), with the sign of what is missing: the odd one.
+// x >= 0, next to a value that is larger by `rest` (or smaller): the odd one of the float32 values around that one.
 __device__ __forceinline__ float made_odd(float x, float rest)
 {
-    const uint32_t u = __builtin_bit_cast(uint32_t, x);
-    const uint32_t off = ((__builtin_bit_cast(uint32_t, rest) ^ u) >> 31) ? ~0u : 1u;   // towards zero or away
-    return __builtin_bit_cast(float, rest != 0.0f && !(u & 1) ? u + off : u);
+    const uint32_t below = __builtin_bit_cast(uint32_t, x) + (uint32_t)(__builtin_bit_cast(int32_t, rest) >> 31);
+    return __builtin_bit_cast(float, below | (rest != 0.0f ? 1u : 0u));
 }
 
-// x / s for the rounding to a code: r is about 1 / s, both at least 2^-60 and x no larger than 2^9 s. (Two
+// |x| / s for the rounding to a code: r is about 1 / s, both at least 2^-62 and |x| no larger than 2^9 s. (Two
 // steps take the quotient to one of its neighbours.)
 __device__ __forceinline__ float quotient(float x, float s, float r)
 {
-    const float q0 = x * r, q = fmaf(-fmaf(q0, s, -x), r, q0);
-    return made_odd(q, -fmaf(q, s, -x));
+    const float q0 = fabsf(x) * r, q = fmaf(fmaf(-q0, s, fabsf(x)), r, q0);
+    return made_odd(q, fmaf(-q, s, fabsf(x)));
 }
 
 template <bool INT8>
@@ -40,17 +39,17 @@ __device__ __forceinline__ float largest()
     return INT8 ? 127.0f : 448.0f;
 }
 
-// Four quotients to codes.
+// Four quotients with their signs to codes.
 template <bool INT8>
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d)
 {
     if constexpr (!INT8) {
         return pack_e4m3(clamp448(a), clamp448(b), clamp448(c), clamp448(d));
-    } else {
-        auto code = [](float x) {
-            return (uint32_t)(int32_t)__builtin_rintf(fminf(fmaxf(x, -127.0f), 127.0f)) & 0xFFu;
-        };
-        return code(a) | code(b) << 8 | code(c) << 16 | code(d) << 24;
+    } else {   // as bytes 1 to 255, and back
+        uint32_t w = __builtin_amdgcn_cvt_pk_u8_f32(__builtin_rintf(a) + 128.0f, 0, 0);
+        w = __builtin_amdgcn_cvt_pk_u8_f32(__builtin_rintf(b) + 128.0f, 1, w);
+        w = __builtin_amdgcn_cvt_pk_u8_f32(__builtin_rintf(c) + 128.0f, 2, w);
+        return __builtin_amdgcn_cvt_pk_u8_f32(__builtin_rintf(d) + 128.0f, 3, w) ^ 0x80808080u;
     }
 }
 
@@ -70,8 +69,8 @@ __device__ __forceinline__ uint32_t larger_pair(uint32_t x, uint32_t y)
                                                                   __builtin_bit_cast(u16x2, y)));
 }
 
-// A wave quantises the runs that start among `range` tokens, for one head and keys or values. Magnitudes are
-// compared as the integers that their bits are, infinities and NaN above all others.
+// A wave quantises the runs that start among `range` tokens (y: the head, z: keys or values). Magnitudes are compared
+// as the integers that their bits are, infinities and NaN above all others.
 constexpr int kPieces = 8;   // 16-byte pieces of a run's rows that a lane holds at a time
 
 template <class Type, bool INT8>
@@ -79,19 +78,18 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
 {
     typedef typename Type::T T;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int32_t block = a.c.block, dim = a.c.dim, per_row = dim / 8;
-    const int kinds = 2 * a.c.heads;
+    const int h = blockIdx.y, s = blockIdx.z;
+    const int64_t t0 = ((int64_t)blockIdx.x * kRowWaves + wave) * range;
+    if (t0 >= a.T)
+        return;
+    const int32_t block = a.c.block, dim = a.c.dim, per_row = dim / 8;   // 8 to 32
+    const uint32_t of_row = (65536 + per_row - 1) / per_row;             // p / per_row = p of_row >> 16 below 2048
     const int64_t slots = (int64_t)a.c.num_pages * a.c.page_size;
     auto slot_of = [&](int64_t t) {
         const int32_t x = t >= 0 && t < a.T ? a.slot_map[t] : -1;
         return x < slots ? x : -1;
     };
     auto follows = [&](int32_t x, int32_t before) { return before >= 0 && x == before + 1 && x % block != 0; };
-    for (int64_t unit = (int64_t)blockIdx.x * (kRowThreads / 64) + wave;; unit += (int64_t)gridDim.x * (kRowThreads / 64)) {
-    const int64_t t0 = unit / kinds * range;
-    const int kind = (int)(unit % kinds), s = kind & 1, h = kind >> 1;
-    if (t0 >= a.T)
-        return;
     const int32_t own = lane < range ? slot_of(t0 + lane) : -1, before = slot_of(t0 + lane - 1);
     uint64_t starts = __ballot(own >= 0 && !follows(own, before));
     while (starts) {
@@ -112,9 +110,9 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
         auto load = [&](int32_t p0) {
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
-                const int32_t p = p0 + 64 * j + lane, row = p / per_row;
+                const uint32_t p = p0 + 64 * j + lane, row = p * of_row >> 16;
                 in[j] = u32x4{0, 0, 0, 0};
-                if (p < pieces)
+                if (p < (uint32_t)pieces)
                     in[j] = *(const u32x4 *)(x + row * a.ld[s] + (p - row * per_row) * 8);
             }
         };
@@ -145,15 +143,17 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
                 load(p0);
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
-                const int32_t p = p0 + 64 * j + lane, row = p / per_row;
-                if (p >= pieces)
+                const uint32_t p = p0 + 64 * j + lane, row = p * of_row >> 16;
+                if (p >= (uint32_t)pieces)
                     continue;
                 union { u32x4 u; T v[8]; } y;
                 y.u = in[j];
                 float q[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    q[e] = quotient(Type::f(y.v[e]) * lift, up, r);
+                for (int e = 0; e < 8; ++e) {
+                    const float v = Type::f(y.v[e]) * lift;
+                    q[e] = copysignf(quotient(v, up, r), v);
+                }
                 u32x2 o = {codes4<INT8>(q[0], q[1], q[2], q[3]), codes4<INT8>(q[4], q[5], q[6], q[7])};
                 if (none)
                     o = u32x2{0, 0};
@@ -164,12 +164,12 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
         if (off && scale > old) {
             const double from = old, to = scale;
             auto again = [&](float code) {
-                const double x = (double)code * from / to;
+                const double x = fabs((double)code * from / to);
                 const float q = (float)x;
-                return made_odd(q, (float)(x - (double)q));
+                return copysignf(made_odd(q, (float)(x - (double)q)), code);
             };
             for (int32_t p = lane; p < block * per_row; p += 64) {
-                const int32_t row = p / per_row;
+                const int32_t row = p * of_row >> 16;
                 if (row >= off && row < off + rows)
                     continue;
                 u32x2 *at = (u32x2 *)(codes + row * a.c.slot[s] + (p - row * per_row) * 8);
@@ -182,44 +182,46 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
             }
         }
     }
-    }
 }
 
-// A thread takes one piece of 16 codes of a slot's row.
+// A thread stays with its piece of 8 values of a token's row and goes over tokens. Rows of more than 256 pieces take
+// several work-groups (z).
 template <class Type, bool INT8>
-__global__ __launch_bounds__(kRowThreads) void quantized_read_kernel(QuantizedRowsArgs a)
+__global__ __launch_bounds__(kRowThreads) void quantized_read_kernel(QuantizedRowsArgs a, uint32_t width)
 {
     typedef typename Type::T T;
     const int s = blockIdx.y;
-    const uint32_t per_row = (uint32_t)a.c.dim / 16, per_token = per_row * (uint32_t)a.c.heads;
-    const int64_t slots = (int64_t)a.c.num_pages * a.c.page_size, all = (int64_t)a.T * per_token;
-    for (int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; i < all; i += (int64_t)gridDim.x * kRowThreads) {
-        const int64_t t = i / per_token;
-        const uint32_t c = (uint32_t)(i - t * per_token), h = c / per_row, d = (c - h * per_row) * 16;
+    const uint32_t per_head = (uint32_t)a.c.dim / 8, per_token = per_head * (uint32_t)a.c.heads;
+    const uint32_t row = threadIdx.x / width, c = blockIdx.z * kRowThreads + (threadIdx.x - row * width);
+    const uint32_t rows = kRowThreads / width;
+    if (row >= rows || c >= per_token)
+        return;
+    const uint32_t h = c / per_head, d = (c - h * per_head) * 8;
+    const int64_t slots = (int64_t)a.c.num_pages * a.c.page_size;
+    const uint8_t *codes = a.c.codes[s] + h * a.c.head[s] + d;
+    const float *scales = a.c.scale[s] + h * a.c.scale_head[s];
+    T *out = (T *)a.x[s] + h * a.hs[s] + d;
+    for (int64_t t = (int64_t)blockIdx.x * rows + row; t < a.T; t += (int64_t)gridDim.x * rows) {
         const int32_t slot = a.slot_map[t];
-        T *to = (T *)a.x[s] + t * a.ld[s] + h * a.hs[s] + d;
-        union { u32x4 u[2]; T v[16]; } out;
-        out.u[0] = out.u[1] = u32x4{0, 0, 0, 0};
+        union { u32x4 u; T v[8]; } o;
+        o.u = u32x4{0, 0, 0, 0};
         if (slot >= 0 && slot < slots) {
             const int32_t page = slot / a.c.page_size, in_page = slot - page * a.c.page_size;
-            const u32x4 w = *(const u32x4 *)(a.c.codes[s] + page * a.c.page[s] + in_page * a.c.slot[s] +
-                                             h * a.c.head[s] + d);
-            const float scale = a.c.scale[s][page * a.c.scale_page[s] + in_page / a.c.block * a.c.scale_block[s] +
-                                             h * a.c.scale_head[s]];
+            const u32x2 w = *(const u32x2 *)(codes + page * a.c.page[s] + in_page * a.c.slot[s]);
+            const float scale = scales[page * a.c.scale_page[s] + in_page / a.c.block * a.c.scale_block[s]];
             auto value = [&](float code) {
-                const float p = code * scale;
-                return Type::from(made_odd(p, fmaf(code, scale, -p)));
+                const float p = fabsf(code * scale);
+                return Type::from(copysignf(made_odd(p, fmaf(fabsf(code), scale, -p)), code));
             };
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                out.v[4 * e] = value(value_of<INT8, 0>(w[e]));
-                out.v[4 * e + 1] = value(value_of<INT8, 1>(w[e]));
-                out.v[4 * e + 2] = value(value_of<INT8, 2>(w[e]));
-                out.v[4 * e + 3] = value(value_of<INT8, 3>(w[e]));
+            for (int e = 0; e < 2; ++e) {
+                o.v[4 * e] = value(value_of<INT8, 0>(w[e]));
+                o.v[4 * e + 1] = value(value_of<INT8, 1>(w[e]));
+                o.v[4 * e + 2] = value(value_of<INT8, 2>(w[e]));
+                o.v[4 * e + 3] = value(value_of<INT8, 3>(w[e]));
             }
         }
-        *(u32x4 *)to = out.u[0];
-        *(u32x4 *)(to + 8) = out.u[1];
+        *(u32x4 *)(out + t * a.ld[s]) = o.u;
     }
 }
 
@@ -227,32 +229,37 @@ __global__ __launch_bounds__(kRowThreads) void quantized_read_kernel(QuantizedRo
 
 hipError_t launch_quantized_write(const QuantizedRowsArgs &a, hipStream_t stream)
 {
-    const int range = 1;
-    const int64_t units = ((int64_t)a.T + range - 1) / range * 2 * a.c.heads;
-    const int64_t blocks = (units + kRowThreads / 64 - 1) / (kRowThreads / 64);
-    const dim3 grid((unsigned)(blocks < 1 << 20 ? blocks : 1 << 20)), block(kRowThreads);
+    // As many tokens to a wave as leave 8 waves per SIMD (1024 of them), 16 at most.
+    int64_t range = (int64_t)a.T * 2 * a.c.heads / 8192;
+    range = range < 1 ? 1 : range > 16 ? 16 : range;
+    const int64_t waves = (a.T + range - 1) / range;
+    const dim3 grid((unsigned)((waves + kRowWaves - 1) / kRowWaves), (unsigned)a.c.heads, 2), block(kRowThreads);
+    const int n = (int)range;
     if (a.c.int8)
-        a.fp16 ? quantized_write_kernel<Fp16, true><<<grid, block, 0, stream>>>(a, range)
-               : quantized_write_kernel<Bf16, true><<<grid, block, 0, stream>>>(a, range);
+        a.fp16 ? quantized_write_kernel<Fp16, true><<<grid, block, 0, stream>>>(a, n)
+               : quantized_write_kernel<Bf16, true><<<grid, block, 0, stream>>>(a, n);
     else
-        a.fp16 ? quantized_write_kernel<Fp16, false><<<grid, block, 0, stream>>>(a, range)
-               : quantized_write_kernel<Bf16, false><<<grid, block, 0, stream>>>(a, range);
+        a.fp16 ? quantized_write_kernel<Fp16, false><<<grid, block, 0, stream>>>(a, n)
+               : quantized_write_kernel<Bf16, false><<<grid, block, 0, stream>>>(a, n);
     return hipGetLastError();
 }
 
 hipError_t launch_quantized_read(const QuantizedRowsArgs &a, int cus, hipStream_t stream)
 {
-    const int64_t all = (int64_t)a.T * a.c.heads * (a.c.dim / 16);
-    int64_t blocks = (all + kRowThreads - 1) / kRowThreads;
-    if (blocks > (int64_t)cus * 16)
-        blocks = (int64_t)cus * 16;
-    const dim3 grid((unsigned)blocks, 2), block(kRowThreads);
+    const int64_t per_token = (int64_t)a.c.heads * (a.c.dim / 8);
+    const uint32_t width = per_token < kRowThreads ? (uint32_t)per_token : kRowThreads, rows = kRowThreads / width;
+    const int64_t slices = (per_token + kRowThreads - 1) / kRowThreads;   // at most 8192: 65535 heads of 256
+    int64_t blocks = ((int64_t)a.T + rows - 1) / rows;
+    const int64_t most = (int64_t)cus * 8 / slices;
+    if (blocks > (most < 1 ? 1 : most))
+        blocks = most < 1 ? 1 : most;
+    const dim3 grid((unsigned)blocks, 2, (unsigned)slices), block(kRowThreads);
     if (a.c.int8)
-        a.fp16 ? quantized_read_kernel<Fp16, true><<<grid, block, 0, stream>>>(a)
-               : quantized_read_kernel<Bf16, true><<<grid, block, 0, stream>>>(a);
+        a.fp16 ? quantized_read_kernel<Fp16, true><<<grid, block, 0, stream>>>(a, width)
+               : quantized_read_kernel<Bf16, true><<<grid, block, 0, stream>>>(a, width);
     else
-        a.fp16 ? quantized_read_kernel<Fp16, false><<<grid, block, 0, stream>>>(a)
-               : quantized_read_kernel<Bf16, false><<<grid, block, 0, stream>>>(a);
+        a.fp16 ? quantized_read_kernel<Fp16, false><<<grid, block, 0, stream>>>(a, width)
+               : quantized_read_kernel<Bf16, false><<<grid, block, 0, stream>>>(a, width);
     return hipGetLastError();
 }
 
