@@ -488,7 +488,7 @@ typedef struct {
  *   touch nothing else).
  *   Where a run's row holds a value that is not finite, the scale becomes NaN and the run's codes zero: the whole
  *   block and head then reads as NaN, until it is started anew.
- *   0 <= T; k, v of `type` W4A16_BF16 or W4A16_FP16, 16-byte aligned, strides multiples of 8.
+ *   0 <= T, T * heads <= 2^35; k, v of `type` W4A16_BF16 or W4A16_FP16, 16-byte aligned, strides multiples of 8.
  */
 w4a16_status_t w4a16_quantized_kv_write(const void *k, int64_t ldk, int64_t hsk, const void *v, int64_t ldv,
                                         int64_t hsv, int32_t T, int32_t type, const int32_t *slot_map,

@@ -109,7 +109,8 @@ def test_caches(call, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(k=None), NULLP), (dict(v=None), NULLP), (dict(slots=None), NULLP), (dict(type=2), TYPE), (dict(type=3), TYPE),
     (dict(T=-1), SHAPE), (dict(k=A + 2), ALIGN), (dict(ldk=516), ALIGN), (dict(hsv=12), ALIGN), (dict(slots=A + 2), ALIGN),
-    (dict(T=0, k=None, v=None, slots=None), DEVICE),
+    (dict(T=0, k=None, v=None, slots=None), DEVICE), (dict(T=2 ** 31 - 1), DEVICE),
+    (dict(c=cache(heads=17), T=2 ** 31 - 1), SHAPE),
 ])
 def test_rows(call, kw, status):
     assert call(**kw) == status

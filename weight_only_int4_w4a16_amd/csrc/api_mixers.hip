@@ -118,7 +118,7 @@ w4a16_status_t check_rows(const void *k, int64_t ldk, int64_t hsk, const void *v
     const w4a16_status_t st = check_quantized(cache);
     if (st != W4A16_OK)
         return st;
-    if (T < 0)
+    if (T < 0 || (int64_t)T * cache->heads > 1LL << 35)
         return W4A16_ERR_BAD_SHAPE;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 4) || !strided8(ldk, hsk) || !strided8(ldv, hsv))
         return W4A16_ERR_MISALIGNED;

@@ -25,26 +25,27 @@ __device__ __forceinline__ float made_odd(float x, float rest)
     return __builtin_bit_cast(float, below | (rest != 0.0f ? 1u : 0u));
 }
 
-// |x| / s for the rounding to a code: r is about 1 / s, both at least 2^-62 and |x| no larger than 2^9 s. (Two
-// steps take the quotient to one of its neighbours.)
-__device__ __forceinline__ float quotient(float x, float s, float r)
-{
-    const float q0 = fabsf(x) * r, q = fmaf(fmaf(-q0, s, fabsf(x)), r, q0);
-    return made_odd(q, fmaf(-q, s, fabsf(x)));
-}
-
 template <bool INT8>
 __device__ __forceinline__ float largest()
 {
     return INT8 ? 127.0f : 448.0f;
 }
 
-// Four quotients with their signs to codes.
+// x / s for the rounding to a code: r is about 1 / s, both at least 2^-62 and |x| no larger than 2^9 s. (Two
+// steps take the quotient to one of its neighbours.)
+template <bool INT8>
+__device__ __forceinline__ float quotient(float x, float s, float r)
+{
+    const float q0 = fabsf(x) * r, q = fmaf(fmaf(-q0, s, fabsf(x)), r, q0);
+    return copysignf(fminf(made_odd(q, fmaf(-q, s, fabsf(x))), largest<INT8>()), x);
+}
+
+// Four quotients, no larger than the largest code, to codes.
 template <bool INT8>
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d)
 {
     if constexpr (!INT8) {
-        return pack_e4m3(clamp448(a), clamp448(b), clamp448(c), clamp448(d));
+        return pack_e4m3(a, b, c, d);
     } else {   // as bytes 1 to 255, and back
         uint32_t w = __builtin_amdgcn_cvt_pk_u8_f32(__builtin_rintf(a) + 128.0f, 0, 0);
         w = __builtin_amdgcn_cvt_pk_u8_f32(__builtin_rintf(b) + 128.0f, 1, w);
@@ -69,8 +70,9 @@ __device__ __forceinline__ uint32_t larger_pair(uint32_t x, uint32_t y)
                                                                   __builtin_bit_cast(u16x2, y)));
 }
 
-// A wave quantises the runs that start among `range` tokens (y: the head, z: keys or values). Magnitudes are compared
-// as the integers that their bits are, infinities and NaN above all others.
+// A wave quantises the runs that start among `range` tokens, of one head (the heads of a token lie next to each other)
+// and keys or values (y). Magnitudes are compared as the integers that their bits are, infinities and NaN above all
+// others.
 constexpr int kPieces = 8;   // 16-byte pieces of a run's rows that a lane holds at a time
 
 template <class Type, bool INT8>
@@ -78,8 +80,10 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
 {
     typedef typename Type::T T;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int h = blockIdx.y, s = blockIdx.z;
-    const int64_t t0 = ((int64_t)blockIdx.x * kRowWaves + wave) * range;
+    const int s = blockIdx.y;
+    const uint32_t unit = blockIdx.x * kRowWaves + wave, part = unit / (uint32_t)a.c.heads;
+    const int h = (int)(unit - part * (uint32_t)a.c.heads);
+    const int64_t t0 = (int64_t)part * range;
     if (t0 >= a.T)
         return;
     const int32_t block = a.c.block, dim = a.c.dim, per_row = dim / 8;   // 8 to 32
@@ -90,8 +94,8 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
         return x < slots ? x : -1;
     };
     auto follows = [&](int32_t x, int32_t before) { return before >= 0 && x == before + 1 && x % block != 0; };
-    const int32_t own = lane < range ? slot_of(t0 + lane) : -1, before = slot_of(t0 + lane - 1);
-    uint64_t starts = __ballot(own >= 0 && !follows(own, before));
+    const int32_t own = slot_of(t0 + lane), behind = slot_of(t0 + 64 + lane), before = slot_of(t0 + lane - 1);
+    uint64_t starts = __ballot(lane < range && own >= 0 && !follows(own, before));
     while (starts) {
         const int i = __builtin_ctzll(starts);
         starts &= starts - 1;
@@ -99,7 +103,8 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
         const int32_t slot = __builtin_amdgcn_readlane(own, i);
         const int32_t page = slot / a.c.page_size, in_page = slot - page * a.c.page_size;
         const int32_t b = in_page / block, off = in_page - b * block;
-        const uint64_t run = __ballot((uint32_t)slot_of(t + lane) == (uint32_t)slot + lane);
+        const int32_t x0 = __shfl(own, lane + i & 63), x1 = __shfl(behind, lane + i & 63);
+        const uint64_t run = __ballot((uint32_t)(lane + i < 64 ? x0 : x1) == (uint32_t)slot + lane);
         const int32_t rows = min(~run ? __builtin_ctzll(~run) : 64, block - off);
         const int32_t pieces = rows * per_row;
         const T *x = (const T *)a.x[s] + h * a.hs[s] + t * a.ld[s];
@@ -138,9 +143,7 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
             *scale_at = scale;
         const bool none = scale != scale;
         const float lift = scale < 0x1p-60f ? 0x1p64f : 1.0f, up = scale * lift, r = 1.0f / up;
-        for (int32_t p0 = 0; p0 < pieces; p0 += 64 * kPieces) {
-            if (pieces > 64 * kPieces)
-                load(p0);
+        auto quantise = [&](int32_t p0, float factor) {
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
                 const uint32_t p = p0 + 64 * j + lane, row = p * of_row >> 16;
@@ -150,15 +153,21 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
                 y.u = in[j];
                 float q[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = Type::f(y.v[e]) * lift;
-                    q[e] = copysignf(quotient(v, up, r), v);
-                }
+                for (int e = 0; e < 8; ++e)
+                    q[e] = quotient<INT8>(Type::f(y.v[e]) * factor, up, r);
                 u32x2 o = {codes4<INT8>(q[0], q[1], q[2], q[3]), codes4<INT8>(q[4], q[5], q[6], q[7])};
                 if (none)
                     o = u32x2{0, 0};
                 *(u32x2 *)(codes + (off + row) * a.c.slot[s] + (p - row * per_row) * 8) = o;
             }
+        };
+        for (int32_t p0 = 0; p0 < pieces; p0 += 64 * kPieces) {
+            if (pieces > 64 * kPieces)
+                load(p0);
+            if (lift == 1.0f)
+                quantise(p0, 1.0f);   // no multiplication
+            else
+                quantise(p0, lift);
         }
         // What the block held goes over to the new scale, in float64 (rare: a block's scale has grown).
         if (off && scale > old) {
@@ -166,7 +175,7 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
             auto again = [&](float code) {
                 const double x = fabs((double)code * from / to);
                 const float q = (float)x;
-                return copysignf(made_odd(q, (float)(x - (double)q)), code);
+                return copysignf(fminf(made_odd(q, (float)(x - (double)q)), largest<INT8>()), code);
             };
             for (int32_t p = lane; p < block * per_row; p += 64) {
                 const int32_t row = p * of_row >> 16;
@@ -232,8 +241,8 @@ hipError_t launch_quantized_write(const QuantizedRowsArgs &a, hipStream_t stream
     // As many tokens to a wave as leave 8 waves per SIMD (1024 of them), 16 at most.
     int64_t range = (int64_t)a.T * 2 * a.c.heads / 8192;
     range = range < 1 ? 1 : range > 16 ? 16 : range;
-    const int64_t waves = (a.T + range - 1) / range;
-    const dim3 grid((unsigned)((waves + kRowWaves - 1) / kRowWaves), (unsigned)a.c.heads, 2), block(kRowThreads);
+    const int64_t waves = (a.T + range - 1) / range * a.c.heads;   // below 2^32: T heads <= 2^35
+    const dim3 grid((unsigned)((waves + kRowWaves - 1) / kRowWaves), 2), block(kRowThreads);
     const int n = (int)range;
     if (a.c.int8)
         a.fp16 ? quantized_write_kernel<Fp16, true><<<grid, block, 0, stream>>>(a, n)
