@@ -172,25 +172,33 @@ __device__ __forceinline__ void tokens_of(const DeltaArgs &a, int s, int32_t *t0
     *t1 = a.cu ? max(__builtin_amdgcn_readfirstlane(min(max(a.cu[s + 1], 0), a.T)), *t0) : a.T;
 }
 
-// The last sequence whose places start at or before `place`, or -1; 64 of them at a time.
-__device__ __forceinline__ int sequence_at(const DeltaArgs &a, int32_t place)
+// The tokens [t0, t1) of the chunk at `place`; false where it is none's. Its sequence is the last one whose places
+// start there or before: 63 are looked through at a time, so that the last look has both of its ends.
+__device__ __forceinline__ bool chunk_at(const DeltaArgs &a, int32_t place, int32_t *t0, int32_t *t1)
 {
-    if (!a.cu)
-        return 0;
-    const int lane = threadIdx.x & 63;
-    int lo = 0, n = a.B;
-    while (n > 0) {
-        const int step = (n + 63) / 64, at = lo + lane * step;
-        const uint64_t hit = __ballot(lane * step < n && first_place(a, at) <= place);
-        if (!hit)
-            return -1;
-        const int k = 63 - __builtin_clzll(hit);
-        if (step == 1)
-            return lo + k;
-        lo += k * step;
-        n = min(step, n - k * step);
+    if (!a.cu) {
+        *t0 = place * kChunk;
+        *t1 = a.T;
+    } else {
+        const int lane = threadIdx.x & 63;
+        for (int lo = 0, n = a.B;;) {
+            const int step = (n + 62) / 63, at = lo + lane * step;
+            const int32_t start = min(max(a.cu[min(at, a.B)], 0), a.T);
+            const uint64_t hit = __ballot(lane * step < n && start / kChunk + at <= place);
+            if (!hit)
+                return false;
+            const int k = 63 - __builtin_clzll(hit);
+            if (step == 1) {
+                const int32_t first = __builtin_amdgcn_readlane(start, k);
+                *t1 = __builtin_amdgcn_readlane(start, k + 1);
+                *t0 = first + (place - first / kChunk - lo - k) * kChunk;
+                break;
+            }
+            lo += k * step;
+            n = min(step, n - k * step);
+        }
     }
-    return -1;
+    return *t0 < *t1;
 }
 
 __device__ __forceinline__ f32x4 mfma_f32(f32x4 a, f32x4 b, f32x4 c)   // contraction of 16, lane group g has 4g ..
@@ -201,28 +209,50 @@ __device__ __forceinline__ f32x4 mfma_f32(f32x4 a, f32x4 b, f32x4 c)   // contra
     return c;
 }
 
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+// x or zero, without the branch around x that a selection becomes.
+__device__ __forceinline__ float masked(float x, bool keep)
+{
+    return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & (keep ? ~0u : 0u));
+}
+
+// Work-groups go to the 8 XCDs in turn, and each XCD has its own L2. Of `groups` that read the same rows, each of
+// `size` work-groups, all of one go to one XCD: group and number inside it of a work-group.
+struct Xcd {
+    uint32_t groups, size;
+    __device__ __forceinline__ bool place(uint32_t block, uint32_t *group, uint32_t *inside) const
+    {
+        const uint32_t rest = block / 8, eight = rest / size;
+        *inside = rest - eight * size;
+        *group = eight * 8 + block % 8;
+        return *group < groups;
+    }
+    int64_t blocks() const { return ((int64_t)groups + 7) / 8 * 8 * size; }
+};
+
 // T and P of one chunk and head. Wave w has rows 16 w ..; products of K rows are formed both ways round, so that
 // each result lies in the lanes where it is an operand. A and T are float32: diagonal blocks of 16 x 16 by
 // substitution (no powers of A, which may be large where T is not), the others by float32 matrix products,
 //   T_ij = -(sum_{j<m<=i} T_im A_mj) T_jj.
 template <class Type, int DK>
-__global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs a, Prepared<Type> *work)
+__global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs a, Prepared<Type> *work, Xcd xcd)
 {
     constexpr int C = DK / 32;
+    __shared__ u32x4 lds_k[kWaves - 1][C][64];
     __shared__ f32x4 lds_a[10][64], lds_t[kWaves][64];
-    __shared__ double lds_b[kChunk];
+    __shared__ __align__(16) double lds_b[kChunk];
     __shared__ __align__(16) float lds_beta[kChunk];
     __shared__ int32_t lds_bad[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int col = lane & 15, g = lane >> 4, h = blockIdx.y, hk = h / (a.H / a.Hk);
-    const int32_t place = (int32_t)blockIdx.x;
-    const int seq = sequence_at(a, place);
-    if (seq < 0)
+    const int col = lane & 15, g = lane >> 4;
+    uint32_t group, inside;   // a place and head of K, heads that share it
+    if (!xcd.place(blockIdx.x, &group, &inside))
         return;
+    const int32_t place = (int32_t)(group / (uint32_t)a.Hk);
+    const int hk = (int)(group - (uint32_t)place * (uint32_t)a.Hk), h = hk * (int)xcd.size + (int)inside;
     int32_t t0, t1;
-    tokens_of(a, seq, &t0, &t1);
-    t0 += (place - first_place(a, seq)) * kChunk;
-    if (t0 >= t1)
+    if (!chunk_at(a, place, &t0, &t1))
         return;
     const int32_t n = min(t1 - t0, kChunk);
     Prepared<Type> &to = work[(int64_t)place * a.H + h];
@@ -261,6 +291,11 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs 
         lds_b[lane] = b;
         lds_beta[lane] = beta;
     }
+    if (w < kWaves - 1) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            lds_k[w][c][lane] = ki[c];
+    }
     __syncthreads();
     int32_t bad = odd_tokens ? __builtin_ctzll(odd_tokens) : kChunk;
 #pragma unroll
@@ -277,7 +312,9 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs 
         }
     }
 
-    const double b_col = lds_b[16 * w + col];
+    const double bi_col = lds_b[16 * w + col];
+    const f64x4 bi = *(const f64x4 *)&lds_b[16 * w + 4 * g];
+    const f32x4 beta_i = *(const f32x4 *)&lds_beta[16 * w + 4 * g];
     f32x4 own = {0.0f, 0.0f, 0.0f, 0.0f};
     u32x4 p[Prepared<Type>::p_terms][2] = {};
 #pragma unroll
@@ -287,7 +324,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs 
         u32x4 kj[C];
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            kj[c] = j == w ? ki[c] : load4(kr, 2 * ((16 * j + col) * (uint32_t)ldk + 32 * c + 8 * g));
+            kj[c] = j == w ? ki[c] : lds_k[min(j, kWaves - 2)][c][lane];
         f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -295,13 +332,14 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs 
             y = mfma(Type(), kj[c], qi[c], y);   // tokens j = 16 j + 4 g .. in the lane of token i = 16 w + col
         }
         const double bj_col = lds_b[16 * j + col];
-        const f32x4 beta_i = *(const f32x4 *)&lds_beta[16 * w + 4 * g];
+        const f64x4 bj = *(const f64x4 *)&lds_b[16 * j + 4 * g];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int32_t i = 16 * w + 4 * g + r, jj = 16 * j + col;
-            x[r] = jj < i && i < lim ? x[r] * __builtin_amdgcn_exp2f((float)(lds_b[i] - bj_col)) * beta_i[r] : 0.0f;
-            const int32_t i2 = 16 * w + col, j2 = 16 * j + 4 * g + r;
-            y[r] = j2 <= i2 && j2 < lim ? y[r] * __builtin_amdgcn_exp2f((float)(b_col - lds_b[j2])) : 0.0f;
+            const float a_ij = x[r] * __builtin_amdgcn_exp2f((float)(bi[r] - bj_col)) * beta_i[r];
+            const float p_ij = y[r] * __builtin_amdgcn_exp2f((float)(bi_col - bj[r]));
+            const int32_t i = 16 * w + 4 * g + r, j2 = 16 * j + 4 * g + r;
+            x[r] = masked(a_ij, (16 * j + col < i) & (i < lim));
+            y[r] = masked(p_ij, (j2 <= 16 * w + col) & (j2 < lim));
         }
         lds_a[w * (w + 1) / 2 + j][lane] = x;
 #pragma unroll
@@ -817,21 +855,22 @@ __device__ __forceinline__ void make_outputs(const DeltaArgs &a, const Prepared<
 constexpr int kChunkThreads = 512;
 
 template <class Type, int DK>
-__global__ __launch_bounds__(kChunkThreads, 2) void delta_chunk_kernel(DeltaArgs a, const Prepared<Type> *work, int slices)
+__global__ __launch_bounds__(kChunkThreads, 4) void delta_chunk_kernel(DeltaArgs a, const Prepared<Type> *work, Xcd xcd,
+                                                                       int heads)
 {
     typedef typename WordsOf<DK / 32>::T Words;
     __shared__ __align__(16) DeltaLds<Words> lds;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // All slices of a head on one XCD (work-groups go to the 8 of them in turn).
-    const uint32_t rest = blockIdx.x / 8, unit = rest / (uint32_t)slices * 8 + blockIdx.x % 8;
-    if (unit >= (uint32_t)a.B * (uint32_t)a.H)   // 2^26 at most
+    uint32_t group, inside;   // `heads` heads of a sequence, their slices
+    if (!xcd.place(blockIdx.x, &group, &inside))
         return;
+    const uint32_t slices = xcd.size / (uint32_t)heads, unit = group * (uint32_t)heads + inside / slices;
     const int seq = (int)(unit / (uint32_t)a.H);
     DeltaUnit d;
     d.unit = unit;
     d.h = (int)(unit - (uint32_t)seq * (uint32_t)a.H);
     d.hk = d.h / (a.H / a.Hk);
-    d.c0 = (int)(rest % slices) * 16;
+    d.c0 = (int)(inside % slices) * 16;
     tokens_of(a, seq, &d.t0, &d.t1);
     const Prepared<Type> *from = work + (int64_t)__builtin_amdgcn_readfirstlane(first_place(a, seq)) * a.H + d.h;
     if (tid < 32)
@@ -853,12 +892,16 @@ template <class Type, int DK>
 hipError_t delta_of(const DeltaArgs &a, hipStream_t stream)
 {
     Prepared<Type> *work = (Prepared<Type> *)a.work;
-    const dim3 block(kDeltaThreads);
-    const int slices = a.Dv / 16;
-    const int64_t units = ((int64_t)a.B * a.H + 7) / 8 * 8;
-    if (a.T > 0)
-        delta_prepare_kernel<Type, DK><<<dim3((unsigned)places(a.T, a.B), a.H), block, 0, stream>>>(a, work);
-    delta_chunk_kernel<Type, DK><<<dim3((unsigned)(units * slices)), dim3(kChunkThreads), 0, stream>>>(a, work, slices);
+    const uint32_t share = (uint32_t)(a.H / a.Hk), slices = (uint32_t)a.Dv / 16;
+    if (a.T > 0) {
+        const Xcd xcd{(uint32_t)(places(a.T, a.B) * a.Hk), share};
+        delta_prepare_kernel<Type, DK><<<dim3((unsigned)xcd.blocks()), dim3(kDeltaThreads), 0, stream>>>(a, work, xcd);
+    }
+    // Heads that share K and Q together, unless that leaves some of the 8 XCDs with more than 5/4 of the average.
+    const uint32_t groups = (uint32_t)a.B * (uint32_t)a.Hk, eights = (groups + 7) / 8;
+    const int heads = eights * 32 <= groups * 5 ? (int)share : 1;
+    const Xcd xcd{(uint32_t)a.B * (uint32_t)a.H / (uint32_t)heads, slices * (uint32_t)heads};
+    delta_chunk_kernel<Type, DK><<<dim3((unsigned)xcd.blocks()), dim3(kChunkThreads), 0, stream>>>(a, work, xcd, heads);
     return hipGetLastError();
 }
 
@@ -866,6 +909,8 @@ hipError_t delta_of(const DeltaArgs &a, hipStream_t stream)
 
 int64_t delta_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t type)
 {
+    if (places(T, num_seqs) * H > 1 << 30)   // 25 TB of them
+        return -1;
     return places(T, num_seqs) * H * (int64_t)(type ? sizeof(Prepared<Fp16>) : sizeof(Prepared<Bf16>));
 }
 
