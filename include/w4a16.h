@@ -421,8 +421,9 @@ w4a16_status_t w4a16_linear_attention_step(const void *q, int64_t ldq, int64_t h
  *   S_t = e^{g_t} S_{t-1} + k_t u_t^T,   u_t = beta_t (v_t - e^{g_t} S_{t-1}^T k_t),   o_t = scale * q_t^T S_t.
  *   beta float: beta_t of head h at beta[t * ldb + h * hsb] (ldb from 0 to 2^24 - 1). Keys of norm 1 and beta from
  *   0 to 2 are meant: with beta |k|^2 above 2 states may grow from token to token.
- *   All else as for w4a16_linear_attention: layouts, strides, decays, cu_seqlens, states (state_out == state_in is
- *   allowed), limits; and num_seqs * H <= 2^26.
+ *   All else as for w4a16_linear_attention: layouts, strides, decays, states (state_out == state_in is allowed),
+ *   limits; num_seqs * H <= 2^26; and cu_seqlens has to be non-decreasing (entries are clamped to [0, T]; tokens and
+ *   states of a list that decreases get undefined values).
  *   States, decays and sums are held in float32 or more, and the operands of all products that reach a state
  *   as sums of three bfloat16 values (24 bits). What reaches the outputs only is rounded to one bfloat16 (the
  *   scores) or two (16 bits; float16 inputs: two everywhere). A k, v, beta or decay that is not finite (a decay

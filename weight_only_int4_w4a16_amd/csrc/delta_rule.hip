@@ -182,16 +182,19 @@ __device__ __forceinline__ bool chunk_at(const DeltaArgs &a, int32_t place, int3
     } else {
         const int lane = threadIdx.x & 63;
         for (int lo = 0, n = a.B;;) {
-            const int step = (n + 62) / 63, at = lo + lane * step;
-            const int32_t start = min(max(a.cu[min(at, a.B)], 0), a.T);
-            const uint64_t hit = __ballot(lane * step < n && start / kChunk + at <= place);
+            const int step = (n + 62) / 63, seq = lo + lane * step;
+            const int32_t start = min(max(a.cu[min(seq, a.B)], 0), a.T);
+            const uint64_t hit = __ballot(lane * step < n && start / kChunk + seq <= place);
             if (!hit)
                 return false;
             const int k = 63 - __builtin_clzll(hit);
             if (step == 1) {
                 const int32_t first = __builtin_amdgcn_readlane(start, k);
                 *t1 = __builtin_amdgcn_readlane(start, k + 1);
-                *t0 = first + (place - first / kChunk - lo - k) * kChunk;
+                const int64_t at = first + (int64_t)(place - first / kChunk - lo - k) * kChunk;
+                if (at >= *t1)
+                    return false;
+                *t0 = (int32_t)at;
                 break;
             }
             lo += k * step;
@@ -501,13 +504,18 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
     const int32_t ldk = (int32_t)a.ldk;
 
     // s[j][r]: row DK / 4 w + EK (4 g + r) + j
-    const int64_t state_at = (d.unit * DK + DK / 4 * w + EK * 4 * g) * a.Dv + d.c0 + col;
+    const int32_t state_at = (DK / 4 * w + EK * 4 * g) * a.Dv + d.c0 + col, state_size = DK * a.Dv;
     f32x4 s[EK];
+    {
+        const Rows from = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(a.state_in + d.unit * state_size), 0,
+                                                            a.state_in ? 4 * state_size : 0, 0x00027000);
 #pragma unroll
-    for (int j = 0; j < EK; ++j)
+        for (int j = 0; j < EK; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            s[j][r] = a.state_in ? a.state_in[state_at + (int64_t)(EK * r + j) * a.Dv] : 0.0f;
+            for (int r = 0; r < 4; ++r)
+                s[j][r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                    from, 4 * (state_at + (EK * r + j) * a.Dv), 0, 0));
+    }
 
     Words kn[kWaves];        // rows 16 i + col, this wave's dims from 4 EK g on
     u32x4 tn[3][2];
@@ -621,18 +629,37 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
         // U of tokens 16 w ..
         const bool odd = __builtin_amdgcn_readfirstlane(lds.odd[parity]) != 0;
         f32x4 u[2];
-        {
-            u32x4 rb[2][3];
+        u32x4 rb[2][3];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                u[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int c = 0; c < 2; ++c) {
+            u[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int term = 0; term < 3; ++term)
-                    rb[c][term] = *(const u32x4 *)lds.r[term][c][lane];
-            }
-            products<3, 3, 2, 2>([&](int c, int term) { return tn[term][c]; },
-                                 [&](int c, int term) { return rb[c][term]; }, u);
+            for (int term = 0; term < 3; ++term)
+                rb[c][term] = *(const u32x4 *)lds.r[term][c][lane];
         }
+        uint32_t kt[16];   // K with tokens in pairs: dims EK col .. of tokens 32 c + 16 x + 4 g + e
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const uint16_t *p = (const uint16_t *)lds.k[w][32 * (e / 8) + 16 * (e / 4 % 2) + 4 * g + e % 4] + EK * col;
+            kt[e] = EK == 2 ? *(const uint32_t *)p : *p;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        products<3, 3, 2, 2>([&](int c, int term) { return tn[term][c]; },
+                             [&](int c, int term) { return rb[c][term]; }, u);
+        u32x4 ka[2][EK][KT];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < EK; ++j) {
+                    uint32_t o[KT];
+                    Split<Type>::of(__builtin_amdgcn_perm(kt[8 * c + 2 * i + 1], kt[8 * c + 2 * i],
+                                                          j ? 0x07060302u : 0x05040100u), o);
+#pragma unroll
+                    for (int term = 0; term < KT; ++term)
+                        ka[c][j][term][i] = o[term];
+                }
         {
             f32x4 y, z;
 #pragma unroll
@@ -651,28 +678,6 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
             lds.bad[parity ^ 1][lane] = kChunk;
             if (lane == 0)
                 lds.odd[parity ^ 1] = 0;
-        }
-        u32x4 ka[2][EK][KT];   // K with tokens in pairs: dims EK col .. of tokens 32 c + 16 x + 4 g + e
-        {
-            uint32_t kt[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const uint16_t *p = (const uint16_t *)lds.k[w][32 * (e / 8) + 16 * (e / 4 % 2) + 4 * g + e % 4] + EK * col;
-                kt[e] = EK == 2 ? *(const uint32_t *)p : *p;
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < EK; ++j) {
-                        uint32_t o[KT];
-                        Split<Type>::of(__builtin_amdgcn_perm(kt[8 * c + 2 * i + 1], kt[8 * c + 2 * i],
-                                                              j ? 0x07060302u : 0x05040100u), o);
-#pragma unroll
-                        for (int term = 0; term < KT; ++term)
-                            ka[c][j][term][i] = o[term];
-                    }
         }
         fetch_t(next);
         __syncthreads();
@@ -715,7 +720,7 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
     for (int j = 0; j < EK; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            a.state_out[state_at + (int64_t)(EK * r + j) * a.Dv] = s[j][r];
+            a.state_out[d.unit * state_size + state_at + (EK * r + j) * a.Dv] = s[j][r];
 }
 
 // Waves 4 to 7 make the outputs, next to the others on their SIMDs: wave 4 + w those of the tokens 16 w .., transposed,
