@@ -1,13 +1,15 @@
 """A hybrid decoder on the library's operators: a linear-attention layer and a paged-attention layer, each
 followed by grouped INT4 experts, over requests of their own lengths.
 
-    python examples/hybrid_decode.py [--requests 4] [--new 8]
+    python examples/hybrid_decode.py [--requests 4] [--new 8] [--delta] [--e4m3 | --int8]
 
 Prompts and single tokens go through the same `forward`: page tables and slots for the new tokens
 (`page_tables`), keys and values into the cache (`paged_kv_write`), attention over it (`paged_attention`, a
 row for every new token with the length that it sees), linear attention (`linear_attention` for prompts,
 `linear_attention_step` for single tokens), and INT4 products for the projections, the experts and the
-head. Weights are random; there are no position codes, as positions enter through the decays and the mask.
+head. With `delta` the linear-attention layer is a gated delta rule (`delta_rule`, `delta_rule_step`); with `block` keys
+and values are held in 8 bits with a scale for each block of that many tokens and head (`quantized_kv_write`,
+`quantized_attention`). Weights are random; there are no position codes, as positions enter through the decays and the mask.
 """
 import argparse
 import os
@@ -21,7 +23,8 @@ import weight_only_int4_w4a16_amd as w  # noqa: E402
 
 class HybridDecoder:
     def __init__(self, hidden=512, heads=8, kv_heads=2, dim=64, experts=8, inner=256, topk=2, vocab=1000,
-                 pages=256, page_size=16, requests=4, longest=512, seed=0, cache_type=torch.bfloat16):
+                 pages=256, page_size=16, requests=4, longest=512, seed=0, cache_type=torch.bfloat16,
+                 delta=False, block=None):
         self.gen = torch.Generator(device="cuda").manual_seed(seed)
         self.heads, self.kv_heads, self.dim, self.topk, self.page_size = heads, kv_heads, dim, topk, page_size
         self.embed = torch.randn(vocab, hidden, device="cuda", generator=self.gen).to(torch.bfloat16)
@@ -37,8 +40,11 @@ class HybridDecoder:
         shape = (pages, kv_heads, page_size, dim)
         self.k_cache, self.v_cache = (torch.zeros(shape, device="cuda").to(cache_type).permute(0, 2, 1, 3)
                                       for _ in range(2))
-        self.scales = {}
-        if cache_type == torch.float8_e4m3fn:
+        self.scales, self.block = {}, block
+        if block is not None:
+            self.scales = dict(k_scale=torch.ones(pages, page_size // block, kv_heads, device="cuda"),
+                               v_scale=torch.ones(pages, page_size // block, kv_heads, device="cuda"))
+        elif cache_type == torch.float8_e4m3fn:
             self.scales = dict(k_scale=torch.full((kv_heads,), 0.02, device="cuda"),
                                v_scale=torch.full((kv_heads,), 0.02, device="cuda"))
         self.table = torch.full((requests, -(-longest // page_size)), -1, dtype=torch.int32, device="cuda")
@@ -46,6 +52,7 @@ class HybridDecoder:
         self.rank = torch.arange(pages, device="cuda")
         self.lens = torch.zeros(requests, dtype=torch.int32, device="cuda")
         self.state = torch.zeros(requests, heads, dim, dim, device="cuda")
+        self.rate = torch.randn(hidden, heads, device="cuda", generator=self.gen) * hidden ** -0.5 if delta else None
 
     def int4(self, rows, cols, experts=None):
         """A random matrix (or one for each expert) in the packed INT4 format."""
@@ -93,7 +100,14 @@ class HybridDecoder:
         q, k, v = self.product(self.linear_in, y).view(T, 3 * heads, dim).split(heads, 1)
         q, k = (torch.nn.functional.normalize(z.float(), dim=-1).to(torch.bfloat16) for z in (q, k))
         decay = torch.nn.functional.logsigmoid(y.float() @ self.gate + 3.0)
-        if max(new_lens) == 1 and min(new_lens) == 1:
+        single = max(new_lens) == 1 and min(new_lens) == 1
+        if self.rate is not None:
+            beta = torch.sigmoid(y.float() @ self.rate)
+            if single:
+                o = w.delta_rule_step(q, k, v, decay, beta, self.state)
+            else:
+                o, _ = w.delta_rule(q, k, v, decay, beta, cu_seqlens=step.cu_new, state=self.state, state_out=self.state)
+        elif single:
             o = w.linear_attention_step(q, k, v, decay, self.state)
         else:
             o, _ = w.linear_attention(q, k, v, decay, cu_seqlens=step.cu_new, state=self.state,
@@ -102,10 +116,14 @@ class HybridDecoder:
         x = x + self.experts(0, self.norm(x))
 
         y = self.product(self.attend_in, self.norm(x)).view(T, heads + 2 * kv, dim)
-        w.paged_kv_write(y[:, heads:heads + kv], y[:, heads + kv:], self.k_cache, self.v_cache, step.slot_map,
-                         **self.scales)
-        o = w.paged_attention(y[:, :heads], self.k_cache, self.v_cache, self.table[row], step.positions + 1,
-                              **self.scales)
+        k, v, cache = y[:, heads:heads + kv], y[:, heads + kv:], (self.k_cache, self.v_cache)
+        if self.block is None:
+            w.paged_kv_write(k, v, *cache, step.slot_map, **self.scales)
+            o = w.paged_attention(y[:, :heads], *cache, self.table[row], step.positions + 1, **self.scales)
+        else:
+            w.quantized_kv_write(k, v, *cache, slot_map=step.slot_map, **self.scales)
+            o = w.quantized_attention(y[:, :heads], *cache, page_table=self.table[row], seq_lens=step.positions + 1,
+                                      **self.scales)
         x = x + self.product(self.attend_out, o.reshape(T, -1))
         x = x + self.experts(1, self.norm(x))
         return self.product(self.head, self.norm(x))
@@ -125,9 +143,12 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--requests", type=int, default=4)
     ap.add_argument("--new", type=int, default=8)
-    ap.add_argument("--e4m3", action="store_true", help="keep keys and values in 8 bits")
+    ap.add_argument("--e4m3", action="store_true", help="keep keys and values in 8 bits, with a scale for each head")
+    ap.add_argument("--int8", action="store_true", help="keep them in 8 bits, with a scale for each 16 tokens and head")
+    ap.add_argument("--delta", action="store_true", help="a gated delta rule in the place of linear attention")
     a = ap.parse_args()
-    model = HybridDecoder(requests=a.requests, cache_type=torch.float8_e4m3fn if a.e4m3 else torch.bfloat16)
+    model = HybridDecoder(requests=a.requests, delta=a.delta, block=16 if a.int8 else None, cache_type=(
+        torch.int8 if a.int8 else torch.float8_e4m3fn if a.e4m3 else torch.bfloat16))
     gen = torch.Generator().manual_seed(1)
     prompts = [torch.randint(0, 1000, (5 + 37 * i % 60,), generator=gen).cuda() for i in range(a.requests)]
     for p, t in zip(prompts, model.generate(prompts, a.new).tolist()):
