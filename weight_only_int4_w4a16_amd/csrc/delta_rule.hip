@@ -561,9 +561,8 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
         from += a.H;
         const Rows next = prepared(t + kChunk);
         // X: this wave's dims
-        Words sb[3], k[kWaves];
         {
-            Words ka[kWaves][KT];
+            Words sb[3], ka[kWaves][KT];
 #pragma unroll
             for (int i = 0; i < NW; ++i) {
                 float x = EK == 2 ? s[0][i] : s[0][2 * i], y = EK == 2 ? s[EK - 1][i] : s[0][2 * i + 1];
@@ -575,11 +574,10 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
 #pragma unroll
             for (int i = 0; i < kWaves; ++i) {
                 x[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                k[i] = kn[i];
 #pragma unroll
                 for (int j = 0; j < NW; ++j) {
                     uint32_t o[KT];
-                    Split<Type>::of(k[i][j], o);
+                    Split<Type>::of(kn[i][j], o);
 #pragma unroll
                     for (int term = 0; term < KT; ++term)
                         ka[i][term][j] = o[term];
@@ -587,6 +585,9 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
             }
             lds.s[0][w][lane] = sb[0];
             lds.s[1][w][lane] = sb[1];
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i)   // for a look at it from the other side
+                lds.k[w][16 * i + col][g] = kn[i];
             products<KT, 3, 2, kWaves>([&](int i, int term) { return ka[i][term]; },
                                        [&](int, int term) { return sb[term]; }, x);
 #pragma unroll
@@ -606,10 +607,6 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
         for (int i = 0; i < kWaves; ++i)
             xs[i] = lds.x[i][w][lane];
         const f32x4 v = lds.v[w][lane];
-        // While these come: K, for a look at it from the other side.
-#pragma unroll
-        for (int i = 0; i < kWaves; ++i)
-            lds.k[w][16 * i + col][g] = k[i];
         __builtin_amdgcn_sched_barrier(0);
         f32x4 x;
 #pragma unroll
@@ -807,6 +804,7 @@ __device__ __forceinline__ void make_outputs(const DeltaArgs &a, const Prepared<
         const float eb = ebn;
         const int32_t bad = __builtin_amdgcn_readfirstlane(badn);
         __syncthreads();
+        __syncthreads();
 
         f32x4 o[kWaves];   // Q S, over the rows of each wave
         {
@@ -826,7 +824,6 @@ __device__ __forceinline__ void make_outputs(const DeltaArgs &a, const Prepared<
             }
         }
         fetch_q(t + kChunk, next);
-        __syncthreads();
         __syncthreads();
 
         const bool odd = __builtin_amdgcn_readfirstlane(lds.odd[parity]) != 0;
