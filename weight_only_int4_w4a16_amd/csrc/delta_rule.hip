@@ -497,10 +497,11 @@ template <class Type, int DK, class Lds>
 __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<Type> *from, const DeltaUnit &d, int w, Lds &lds)
 {
     constexpr int EK = DK / 64, NW = 2 * EK, KT = Split<Type>::terms, PT = Prepared<Type>::p_terms;
+    constexpr int SIDE = KT == 1 ? kWaves : 2;   // tiles of X side by side, as many as registers allow
     typedef typename WordsOf<NW>::T Words;
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int32_t t0 = d.t0, t1 = d.t1;
-    const uint16_t *kp = (const uint16_t *)a.k + d.hk * a.hsk;
+    const uint16_t *k_rows = (const uint16_t *)a.k + d.hk * a.hsk;
     const int32_t ldk = (int32_t)a.ldk;
 
     // s[j][r]: row DK / 4 w + EK (4 g + r) + j
@@ -522,7 +523,7 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
     f32x4 ebn, edn;
     u32x2 endn = {kChunk, 0};
     auto fetch_k = [&](int32_t t) {
-        const Rows kr = rows_of(kp + (int64_t)t * ldk, t1 - t, ldk, DK, 2);
+        const Rows kr = rows_of(k_rows + (int64_t)t * ldk, t1 - t, ldk, DK, 2);
 #pragma unroll
         for (int i = 0; i < kWaves; ++i)
             kn[i] = WordsOf<NW>::load(kr, 2 * ((16 * i + col) * (uint32_t)ldk + DK / 4 * w + 4 * EK * g));
@@ -562,7 +563,7 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
         const Rows next = prepared(t + kChunk);
         // X: this wave's dims
         {
-            Words sb[3], ka[kWaves][KT];
+            Words sb[3];
 #pragma unroll
             for (int i = 0; i < NW; ++i) {
                 float x = EK == 2 ? s[0][i] : s[0][2 * i], y = EK == 2 ? s[EK - 1][i] : s[0][2 * i + 1];
@@ -570,29 +571,35 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
                 for (int term = 0; term < 3; ++term)
                     sb[term][i] = take(Bf16(), x, y);
             }
-            f32x4 x[kWaves];
-#pragma unroll
-            for (int i = 0; i < kWaves; ++i) {
-                x[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int j = 0; j < NW; ++j) {
-                    uint32_t o[KT];
-                    Split<Type>::of(kn[i][j], o);
-#pragma unroll
-                    for (int term = 0; term < KT; ++term)
-                        ka[i][term][j] = o[term];
-                }
-            }
             lds.s[0][w][lane] = sb[0];
             lds.s[1][w][lane] = sb[1];
 #pragma unroll
             for (int i = 0; i < kWaves; ++i)   // for a look at it from the other side
                 lds.k[w][16 * i + col][g] = kn[i];
-            products<KT, 3, 2, kWaves>([&](int i, int term) { return ka[i][term]; },
-                                       [&](int, int term) { return sb[term]; }, x);
 #pragma unroll
-            for (int i = 0; i < kWaves; ++i)
-                lds.x[w][i][lane] = x[i];
+            for (int i0 = 0; i0 < kWaves; i0 += SIDE) {
+                Words ka[SIDE][KT];
+                f32x4 x[SIDE];
+#pragma unroll
+                for (int i = 0; i < SIDE; ++i) {
+                    x[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int j = 0; j < NW; ++j) {
+                        uint32_t o[KT];
+                        Split<Type>::of(kn[i0 + i][j], o);
+#pragma unroll
+                        for (int term = 0; term < KT; ++term)
+                            ka[i][term][j] = o[term];
+                    }
+                }
+                products<KT, 3, 2, SIDE>([&](int i, int term) { return ka[i][term]; },
+                                         [&](int, int term) { return sb[term]; }, x);
+#pragma unroll
+                for (int i = 0; i < SIDE; ++i)
+                    lds.x[w][i0 + i][lane] = x[i];
+                if (SIDE < kWaves)
+                    __builtin_amdgcn_sched_barrier(0);
+            }
         }
         fetch_k(t + kChunk);
         __syncthreads();
@@ -643,20 +650,14 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
         __builtin_amdgcn_sched_barrier(0);
         products<3, 3, 2, 2>([&](int c, int term) { return tn[term][c]; },
                              [&](int c, int term) { return rb[c][term]; }, u);
-        u32x4 ka[2][EK][KT];
+        u32x4 kp[2][EK];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < EK; ++j) {
-                    uint32_t o[KT];
-                    Split<Type>::of(__builtin_amdgcn_perm(kt[8 * c + 2 * i + 1], kt[8 * c + 2 * i],
-                                                          j ? 0x07060302u : 0x05040100u), o);
-#pragma unroll
-                    for (int term = 0; term < KT; ++term)
-                        ka[c][j][term][i] = o[term];
-                }
+                for (int j = 0; j < EK; ++j)
+                    kp[c][j][i] = __builtin_amdgcn_perm(kt[8 * c + 2 * i + 1], kt[8 * c + 2 * i], j ? 0x07060302u : 0x05040100u);
         {
             f32x4 y, z;
 #pragma unroll
@@ -681,13 +682,7 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
 
         // S
         {
-            u32x4 ub[2][3];
             f32x4 sum[2 * EK];   // of each half of the chunk
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int term = 0; term < 3; ++term)
-                    ub[c][term] = *(const u32x4 *)lds.u[term][c][lane];
 #pragma unroll
             for (int j = 0; j < EK; ++j)
 #pragma unroll
@@ -695,8 +690,31 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
                     sum[j][r] = s[j][r] * whole;
                     sum[EK + j][r] = 0.0f;
                 }
-            products<KT, 3, 2, 2 * EK>([&](int x, int term) { return ka[x / EK][x % EK][term]; },
-                                       [&](int x, int term) { return ub[x / EK][term]; }, sum);
+            constexpr int HALVES = KT == 1 ? 2 : 1;   // side by side
+#pragma unroll
+            for (int c0 = 0; c0 < 2; c0 += HALVES) {
+                u32x4 ub[HALVES][3], ka[HALVES][EK][KT];
+#pragma unroll
+                for (int c = 0; c < HALVES; ++c) {
+#pragma unroll
+                    for (int term = 0; term < 3; ++term)
+                        ub[c][term] = *(const u32x4 *)lds.u[term][c0 + c][lane];
+#pragma unroll
+                    for (int j = 0; j < EK; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t o[KT];
+                            Split<Type>::of(kp[c0 + c][j][i], o);
+#pragma unroll
+                            for (int term = 0; term < KT; ++term)
+                                ka[c][j][term][i] = o[term];
+                        }
+                }
+                products<KT, 3, 2, HALVES * EK>([&](int x, int term) { return ka[x / EK][x % EK][term]; },
+                                                [&](int x, int term) { return ub[x / EK][term]; }, sum + c0 * EK);
+                if (HALVES == 1)
+                    __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
             for (int j = 0; j < EK; ++j)
 #pragma unroll
