@@ -70,6 +70,21 @@ __device__ __forceinline__ uint32_t larger_pair(uint32_t x, uint32_t y)
                                                                   __builtin_bit_cast(u16x2, y)));
 }
 
+// The largest of all lanes: rotated inside rows of 16, then rows swapped.
+template <int ROTATE>
+__device__ __forceinline__ uint32_t rotated_max(uint32_t x)
+{
+    return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + ROTATE, 0xF, 0xF, true));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x)
+{
+    x = rotated_max<1>(rotated_max<2>(rotated_max<4>(rotated_max<8>(x))));
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = max(r[0], r[1]);
+    const auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return max(s[0], s[1]);
+}
+
 // A wave quantises the runs that start among `range` tokens, of one head (the heads of a token lie next to each other)
 // and keys or values (y). Magnitudes are compared as the integers that their bits are, infinities and NaN above all
 // others.
@@ -130,9 +145,7 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
                 for (int e = 0; e < 4; ++e)
                     most = larger_pair(most, in[j][e] & 0x7FFF7FFFu);
         }
-        most = max(most & 0xFFFFu, most >> 16);
-        for (int d = 1; d < 64; d <<= 1)
-            most = max(most, (uint32_t)__shfl_xor((int)most, d));
+        most = wave_max(max(most & 0xFFFFu, most >> 16));
         const float amax = Type::f(__builtin_bit_cast(T, (uint16_t)most));
         float scale = fmaxf(amax / largest<INT8>(), kLeast);
         if (off)
