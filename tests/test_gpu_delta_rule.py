@@ -304,3 +304,63 @@ def test_both_ways_into_the_library_and_another_stream():
         x.run(beta=x.beta[:5].cuda())
     with pytest.raises(TypeError, match="beta"):
         x.run(beta=x.beta.double().cuda())
+
+
+def test_offsets_past_32_bits():
+    n, ld = 130, 2 ** 24 - 8   # the longest strides: a chunk's rows lie up to 2^31 bytes apart
+    x = Delta([n], 2, 1, 128, 64, seed=990)
+
+    def far(t, dtype):
+        big = torch.empty((n - 1) * ld + t[0].numel(), dtype=dtype, device="cuda")
+        return big.as_strided(t.shape, (ld,) + t.stride()[1:])
+
+    kw = {}
+    for name in ("q", "k", "v", "g", "beta"):
+        t = getattr(x, name)
+        kw[name] = far(t, t.dtype)
+        kw[name].copy_(t)
+    out = far(x.v, x.dtype)
+    x.check(*x.run(out=out, **kw))
+
+
+@pytest.mark.parametrize("n", [1, 70, 130])
+@pytest.mark.parametrize("ld", [0, 8, 40])
+def test_rows_that_share_memory(n, ld):
+    """Rows closer than their length, or all in one place: rows behind the sequence's end are read as well, and count
+    for nothing."""
+    x = Delta([n], 1, 1, 64, 64, seed=n + ld, norm=0.2)
+
+    def close(t, width):
+        big = (torch.randn((n + 63) * ld + width, generator=torch.Generator().manual_seed(ld)) * 0.1).to(t.dtype)
+        big[(n - 1) * ld + width:] = math.nan                     # not the sequence's
+        return big.as_strided((n, 1, width), (ld, width, 1))
+
+    x.q, x.k, x.v = (close(t, 64) for t in (x.q, x.k, x.v))
+    dev = []
+    for t in (x.q, x.k, x.v):
+        big = torch.empty((n + 63) * ld + 64, dtype=t.dtype, device="cuda")
+        big.copy_(t.as_strided((big.numel(),), (1,)))
+        dev.append(big.as_strided((n, 1, 64), (ld, 64, 1)))
+    x.check(*x.run(q=dev[0], k=dev[1], v=dev[2]))
+
+
+def test_two_streams_at_once():
+    """Calls side by side with workspaces of their own."""
+    xs = [Delta([300, 70], 4, 2, 128, 64, seed=s) for s in (1, 2)]
+    want = [x.run() for x in xs]
+    dev = [[t.cuda() for t in (x.q, x.k, x.v, x.g, x.beta, x.state)] for x in xs]
+    cu = ints([0, 300, 370])
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [w.delta_rule(*d[:5], cu_seqlens=cu, state=d[5], stream=s) for d, s in zip(dev, streams)]
+        torch.cuda.synchronize()
+        for (o, s), (o2, s2) in zip(got, want):
+            assert torch.equal(o, o2) and torch.equal(s, s2)
+
+
+def test_heads_on_every_place():
+    """Head counts that the 8 XCDs divide and do not divide, shared and own keys, one sequence and several."""
+    for lens, H, Hk in [([70], 1, 1), ([70], 3, 3), ([65, 2], 6, 2), ([66], 16, 2), ([5, 70, 1], 8, 8), ([70], 24, 8), ([64] * 9, 2, 1)]:
+        x = Delta(lens, H, Hk, 64, 64, seed=H + Hk)
+        x.check(*x.run())

@@ -224,3 +224,44 @@ def test_strides_ways_in_and_streams():
         w.quantized_attention(x.q.cuda(), dev[0], dev[1][:1], *scales, table, ints(x.lens))
     with pytest.raises(w.W4A16Error):
         w.quantized_attention(x.q.cuda(), *dev, *scales, table, ints(x.lens), workspace=work[:16])
+
+
+def test_offsets_past_32_bits():
+    """Pages whose first element lies past 2^32, in a cache of 2^21 pages."""
+    page, D = 16, 128
+    k = torch.zeros(1 << 21, page, 1, D, dtype=I8, device="cuda")
+    scale = torch.zeros(1 << 21, 1, 1, device="cuda")
+    last = [(1 << 21) - 1, (1 << 21) - 2, 1 << 20]
+    gen = torch.Generator().manual_seed(1)
+    x, s = torch.randint(-127, 128, (48, D), generator=gen, dtype=I8), torch.rand(3, generator=gen) * 0.02 + 0.01
+    for i, p in enumerate(last):
+        k[p, :, 0] = x[16 * i:16 * i + 16].cuda()
+        scale[p] = float(s[i])
+    q = torch.randn(1, 4, D, generator=gen).to(BF)
+    out = w.quantized_attention(q.cuda(), k, k, scale, scale, ints([last]), ints([40]), scale=0.09)
+    rows = (x.double() * s.double().repeat_interleave(16)[:, None])[:40, None]
+    o, _, mag, qk, top = mo.attention(q[0].double(), rows, rows, 0.09)
+    tol, _ = qo.attention_bounds(BF, o, mag, qk, top, 40, D, float(s.max()), 127.0)
+    assert bool(((out[0].cpu().double() - o).abs() <= tol).all())
+
+
+def test_graph_with_lengths_that_grow():
+    """One captured call, replayed while requests grow, begin and end."""
+    x = Attend([300, 5, 0, 64], 4, 2, 64, 32, 32, seed=12)
+    dev, scales, table = x.device(), [s.cuda() for s in x.scale], x.table.cuda()
+    q, lens = x.q.cuda(), ints([1, 5, 0, 0])
+    out, work = torch.empty_like(q), w.quantized_attention_workspace(q, dev[0])
+
+    def call(**kw):
+        return w.quantized_attention(q, *dev, *scales, table, lens, **kw)
+
+    call(out=out, workspace=work)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(out=out, workspace=work)
+    for now in ([1, 5, 0, 0], [300, 0, 0, 64], [129, 5, 0, 1], [0, 0, 0, 0], [300, 5, 0, 64]):
+        lens.copy_(ints(now))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, call())

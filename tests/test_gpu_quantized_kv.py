@@ -265,3 +265,51 @@ def test_ways_in_streams_and_refusals():
         w.quantized_kv_read(*c.dev, *c.dev_scale, ints([0]), dtype=torch.float32)
     with pytest.raises(TypeError, match="k_cache"):
         w.quantized_kv_read(k[None].cuda(), k[None].cuda(), *c.dev_scale, ints([0]))
+
+
+def test_runs_that_meet_in_a_block_touch_nothing_else():
+    """What their block then holds is not said; all other blocks and heads are as they were."""
+    c = Cache(4, 32, 2, 64, 16, torch.int8, seed=15)
+    before = [x.clone() for x in c.dev + c.dev_scale]
+    k, v = rows(6, 2, 64, BF, seed=15)
+    w.quantized_kv_write(k.cuda(), v.cuda(), *c.dev, *c.dev_scale, ints([40, 41, 45, 40, 33, 40]))
+    for x, y in zip(c.dev + c.dev_scale, before):
+        if x.dim() == 4:
+            x, y = x.reshape(8, 16, 2, 64), y.reshape(8, 16, 2, 64)
+        else:
+            x, y = x.reshape(8, 2), y.reshape(8, 2)
+        rest = [0, 1, 3, 4, 5, 6, 7]
+        assert torch.equal(x[rest], y[rest])
+
+
+def test_graph_of_a_step():
+    """A captured write and read, replayed over slots that move on, against the same calls made eagerly."""
+    a, b = (Cache(6, 16, 2, 64, 16, torch.float8_e4m3fn, seed=16) for _ in range(2))
+    k, v = (t.cuda() for t in rows(3, 2, 64, BF, seed=16))
+    slots = ints([16, 40, -1])
+    out = tuple(torch.empty(96, 2, 64, dtype=BF, device="cuda") for _ in range(2))
+    every = ints(list(range(96)))
+
+    def step(c):
+        w.quantized_kv_write(k, v, *c.dev, *c.dev_scale, slots)
+        return w.quantized_kv_read(*c.dev, *c.dev_scale, every, out=out)
+
+    keep = [x.clone() for x in a.dev + a.dev_scale]
+    step(a)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(a)
+    for x, y in zip(a.dev + a.dev_scale, keep):
+        x.copy_(y)
+    for i in range(5):
+        g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        want = step(b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert all(torch.equal(x.float(), y.float()) for x, y in zip(a.dev + a.dev_scale, b.dev + b.dev_scale))
+        slots += torch.tensor([1, 1, 0], dtype=torch.int32, device="cuda")
+        k.mul_(-1.5)
+        v.mul_(1.25)
