@@ -12,6 +12,10 @@ namespace {
 // The state is read once, updated in registers and written once: 8 bytes of HBM traffic per element and nothing
 // else of that order. Both products with the old state, k^T S and q^T S, come from one pass over the registers and
 // one sum over the row groups; with d = e^g they give u = beta (v - d S^T k) and o = d S^T q + (q . k) u.
+//
+// As for linear attention's single token, 32 columns to a work-group below 128 of (request, head), a whole state
+// and streaming loads and stores from there on: 1 request of 32 heads 3.9 us, 250 requests 174 to 185 us (5.7 to 6.1
+// TB/s).
 constexpr int kStepThreads = 256;
 
 template <class Type, int DK, int DV, int CV, bool STREAM>
@@ -136,6 +140,23 @@ void step_typed(const DeltaArgs &a, hipStream_t stream)
 //   S  <- e^{b_63} S + K^T diag(e^{b_63 - b}) U
 // What does not need S comes first, for all chunks side by side: T = (1 + A)^-1 diag(beta) and P, 64 x 64 each. Then
 // a work-group per sequence, head and 16 columns of V goes from chunk to chunk: X = K S, R = V - diag(e^b) X, U = T R.
+//
+// Roundings. Everything but P reaches the state, so S, R, T and e^(b_63 - b) U enter their products (16x16x32, bfloat16)
+// as sums of three bfloat16 values, of which the products above 2^-24 of the whole are taken: 3 where K, which is
+// bfloat16, is the other operand, 6 for T R. float32 products would take 16 times a bfloat16 one's time. Float16 K and Q
+// are sums of two (5 products); with float16 operands the state's columns would need factors of their own, found
+// from chunk to chunk. The outputs take two values of S and U, and P as one (float16: two). Errors against float64 over
+// 20000 tokens: states 1.0e-7 of the norm (in float32 throughout 1.4e-7), outputs 2.2e-3 (their own rounding 1.66e-3).
+// Decays are summed in float64, and differences of sums taken there.
+//
+// What bounds it: 20000 tokens of 32 heads of 128 (16 for q and k) take 104 us for T and P (0.42 GB: 4.0 TB/s, where a
+// copy of 4 GiB reaches 4.7) and 560 us for the chunks, a chain of 313 steps of 4050 cycles (1.4 us where 8 heads
+// leave most CUs idle). Of those the carrying waves spend 1040 on X, 540 on R, 1290 on U and 615 on S, and 570 at the
+// three barriers between; their 36 products take 580, the rest are trips through LDS (182 KB a step, 1450 cycles of its
+// time) and the splitting of values. Most of it is latency, which a second work-group on the CU overlaps
+// where there are more than 32 heads. What had counted before: loads of 4 and 2 bytes (K's other view through LDS: a
+// step 2.1 -> 1.9 us), outputs made by the carrying waves (2.4 -> 2.2), a wait for all loads in flight in every round
+// (2.7 -> 2.4), and 35 spilled registers (float16: 3.9 -> 2.1).
 constexpr int kDeltaThreads = 256, kWaves = 4;
 constexpr int kFrags = 6;   // operands of a lower triangle: rows 16 w.., columns 32 c.. (c <= w / 2)
 __device__ __forceinline__ constexpr int frag(int w, int c) { return w < 2 ? w : 2 * w - 2 + c; }
@@ -238,6 +259,8 @@ struct Xcd {
 // each result lies in the lanes where it is an operand. A and T are float32: diagonal blocks of 16 x 16 by
 // substitution (no powers of A, which may be large where T is not), the others by float32 matrix products,
 //   T_ij = -(sum_{j<m<=i} T_im A_mj) T_jj.
+// (K of the other waves through LDS, sums of decays by vectors: 140 -> 117 us for 10016 of them; heads that share K on
+// one XCD: 107.) Alone it takes 7 us, most of it latency: bounds, rows, 15 steps of substitution, 9 products in turn.
 template <class Type, int DK>
 __global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs a, Prepared<Type> *work, Xcd xcd)
 {
