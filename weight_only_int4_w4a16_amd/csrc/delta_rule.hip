@@ -149,14 +149,15 @@ void step_typed(const DeltaArgs &a, hipStream_t stream)
 // 20000 tokens: states 1.0e-7 of the norm (in float32 throughout 1.4e-7), outputs 2.2e-3 (their own rounding 1.66e-3).
 // Decays are summed in float64, and differences of sums taken there.
 //
-// What bounds it: 20000 tokens of 32 heads of 128 (16 for q and k) take 104 us for T and P (0.42 GB: 4.0 TB/s, where a
-// copy of 4 GiB reaches 4.7) and 560 us for the chunks, a chain of 313 steps of 4050 cycles (1.4 us where 8 heads
-// leave most CUs idle). Of those the carrying waves spend 1040 on X, 540 on R, 1290 on U and 615 on S, and 570 at the
-// three barriers between; their 36 products take 580, the rest are trips through LDS (182 KB a step, 1450 cycles of its
-// time) and the splitting of values. Most of it is latency, which a second work-group on the CU overlaps
-// where there are more than 32 heads. What had counted before: loads of 4 and 2 bytes (K's other view through LDS: a
-// step 2.1 -> 1.9 us), outputs made by the carrying waves (2.4 -> 2.2), a wait for all loads in flight in every round
-// (2.7 -> 2.4), and 35 spilled registers (float16: 3.9 -> 2.1).
+// What bounds it: 20000 tokens of 32 heads of 128 (16 for q and k) take 109 us for T and P (0.41 GB: 3.8 TB/s, where a
+// copy of 4 GiB reaches 4.7) and 590 us for the chunks (medians of a trace; 656 us for both by events), a chain of 313
+// steps. A copy with the cycle counter read between phases showed 4060 cycles a step in the carrying waves: 1040 on X,
+// 540 on R, 1290 on U, 615 on S and 570 at the three barriers between. By count, their 36 products would take 580 and
+// the 182 KB that a step moves through LDS 1450 at 128 bytes a cycle; the rest is latency. 8 heads, which leave most
+// CUs idle, take 474 us, little less than 32. Steps that counted, whole calls of this size: outputs by waves of their
+// own together with K's other view through LDS and pieces of 8 bytes for V and the outputs 982 -> 720 us; loads before
+// barriers rather than in a phase's middle 781 -> 692 on the way there; S read for the outputs after R and K turned
+// early 661 -> 656; 16 spilled registers in float16 1513 -> 781.
 constexpr int kDeltaThreads = 256, kWaves = 4;
 constexpr int kFrags = 6;   // operands of a lower triangle: rows 16 w.., columns 32 c.. (c <= w / 2)
 __device__ __forceinline__ constexpr int frag(int w, int c) { return w < 2 ? w : 2 * w - 2 + c; }
@@ -260,7 +261,7 @@ struct Xcd {
 // substitution (no powers of A, which may be large where T is not), the others by float32 matrix products,
 //   T_ij = -(sum_{j<m<=i} T_im A_mj) T_jj.
 // (K of the other waves through LDS, sums of decays by vectors: 140 -> 117 us for 10016 of them; heads that share K on
-// one XCD: 107.) Alone it takes 7 us, most of it latency: bounds, rows, 15 steps of substitution, 9 products in turn.
+// one XCD: 107.) Alone, for one chunk, it takes 7.5 us: a chain of loads, 15 steps of substitution and 9 products in turn.
 template <class Type, int DK>
 __global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs a, Prepared<Type> *work, Xcd xcd)
 {

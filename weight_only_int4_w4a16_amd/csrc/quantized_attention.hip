@@ -15,11 +15,10 @@
 // weights is the running maximum of s_j + log vs_b, less 15 powers of two (11 bits down to 2^-29 of the largest
 // one). The weights' own sum has another reference, the maximum of s_j, and is held in float32 without rounding.
 //
-// The cache's bytes bound it. 64 ragged requests of up to 8192 positions, 64 heads on 8 of 128, int8: 78 us and 5 joining,
-// 83 in all (0.44 GB: 5.6 TB/s here, where a streaming read of 4 GiB reaches 6.3); one request of 131000 positions 53
-// and 7 us, of 1100 6.7 and 4; 48 requests of up to 5000, e4m3, 26 and 5. Three work-groups per CU 87 us instead
-// of 84.5, four 133; V a tile ahead as well as K 86 instead of 85 (by events). The vector units are busy for half of
-// the time, so the second exponential costs nothing.
+// The cache's bytes bound it. 64 ragged requests of up to 8192 positions, 64 heads on 8 of 128, int8: 82 us and 5 joining
+// (medians of a trace; 83 in all by events; 0.44 GB: 5.3 TB/s here, where a streaming read of 4 GiB reaches 6.3); one
+// request of 131000 positions 54 and 8 us, of 1100 6.8 and 4; 48 requests of up to 5000, e4m3, 26 and 5. By events,
+// three work-groups per CU 87.9 us instead of 84.9, four 133; V a tile ahead as well as K 86 instead of 85.
 #include "attention_runs.h"
 
 namespace w4a16 {

@@ -3,8 +3,8 @@
 //   write: s' = max(amax / Q, 2^-126, s), code = x / s' to the nearest code; where a block's scale grows, what it
 //   held becomes code * s / s'.     read: code * s, rounded once.
 // Both are bound by memory: 2 bytes read and 1 written per value, or 1 and 2.
-// Measured with 8 heads of 128: 12257 tokens of 40 requests written as e4m3 26.5 us (2.8 TB/s: a wave's slots, rows,
-// maximum and stores come one after the other, and the vector units are busy for half of the time), 15 tokens 4.4 us;
+// Measured with 8 heads of 128: 12257 tokens of 40 requests written as e4m3 27 us (2.8 TB/s: a wave's slots, rows,
+// maximum and stores come one after the other, and counters show the vector units busy for 48 % of it), 15 tokens 4.7 us;
 // 60000 tokens read 84 us (4.4 TB/s, where a copy of 4 GiB reaches 4.7), 500 of 4 heads 3 us.
 //
 // Roundings go by the exact quotients and products. Scales come from the values, so quotients on a border
@@ -255,8 +255,8 @@ __global__ __launch_bounds__(kRowThreads) void quantized_read_kernel(QuantizedRo
 hipError_t launch_quantized_write(const QuantizedRowsArgs &a, hipStream_t stream)
 {
     // As many tokens to a wave as leave 8 waves per SIMD (1024 of them), 16 at most: prompts of 12257 tokens with 4, 8,
-    // 16 and 32 to a wave 41, 35, 30 and 30 us at that step (a wave without a run's start costs its launch), while
-    // single tokens of many requests, each a run, want waves of their own.
+    // 16 and 32 to a wave 40.7, 35.2, 30.2 and 30.3 us (the least of 6, before later steps), while single tokens of
+    // many requests, each a run, want waves of their own.
     int64_t range = (int64_t)a.T * 2 * a.c.heads / 8192;
     range = range < 1 ? 1 : range > 16 ? 16 : range;
     const int64_t waves = (a.T + range - 1) / range * a.c.heads;   // below 2^32: T heads <= 2^35
