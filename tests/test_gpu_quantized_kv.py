@@ -227,6 +227,21 @@ def test_large_calls():
     assert not bool(codes[:, :pages - T // page - 1].any())
 
 
+def test_more_threads_than_one_axis_holds():
+    """2^26 tokens of 17 heads, one row for all, most of them with no slot."""
+    T, heads = 1 << 26, 17
+    c = Cache(3, 16, heads, 64, 16, torch.int8, seed=21)
+    k, v = rows(1, heads, 64, BF, seed=21)
+    slots = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    slots[5], slots[T // 2], slots[T - 1] = 0, 16, 32
+    w.quantized_kv_write(k.cuda().expand(T, -1, -1), v.cuda().expand(T, -1, -1), *c.dev, *c.dev_scale, slots)
+    got = w.quantized_kv_read(*c.dev, *c.dev_scale, ints([0, 16, 32]))
+    small = Cache(3, 16, heads, 64, 16, torch.int8, seed=21)
+    small.write(k.expand(3, -1, -1), v.expand(3, -1, -1), [0, 16, 32])
+    want = w.quantized_kv_read(*small.dev, *small.dev_scale, ints([0, 16, 32]))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("T", [1, 2, 17, 1000])
 def test_many_runs(T):
     """Every token in a block of its own, and runs that cross all places of a wave's share of the tokens."""

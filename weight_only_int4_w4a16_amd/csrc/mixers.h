@@ -1,5 +1,6 @@
 // Arguments and launchers of the token mixers: page tables, paged cache writes, paged attention, linear
-// attention, the gated delta rule, and the cache with a scale for each block of tokens and head. The entry points have checked every argument before a launcher sees it.
+// attention, the gated delta rule, and the cache with a scale for each block of tokens and head. The entry points have
+// checked every argument before a launcher sees it.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -19,6 +19,7 @@ namespace w4a16 {
 namespace {
 
 constexpr int kRowThreads = 256, kRowWaves = kRowThreads / 64;
+constexpr int kWide = 22;   // blocks along x, of which a launch holds fewer than 2^32 threads
 constexpr float kLeast = 0x1p-126f;
 
 // x >= 0, next to a value that is larger by `rest` (or smaller): the odd one of the float32 values around that one.
@@ -99,7 +100,7 @@ __global__ __launch_bounds__(kRowThreads) void quantized_write_kernel(QuantizedR
     typedef typename Type::T T;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int s = blockIdx.y;
-    const uint32_t unit = blockIdx.x * kRowWaves + wave, part = unit / (uint32_t)a.c.heads;
+    const uint32_t unit = (blockIdx.z << kWide | blockIdx.x) * kRowWaves + wave, part = unit / (uint32_t)a.c.heads;
     const int h = (int)(unit - part * (uint32_t)a.c.heads);
     const int64_t t0 = (int64_t)part * range;
     if (t0 >= a.T)
@@ -260,7 +261,8 @@ hipError_t launch_quantized_write(const QuantizedRowsArgs &a, hipStream_t stream
     int64_t range = (int64_t)a.T * 2 * a.c.heads / 8192;
     range = range < 1 ? 1 : range > 16 ? 16 : range;
     const int64_t waves = (a.T + range - 1) / range * a.c.heads;   // below 2^32: T heads <= 2^35
-    const dim3 grid((unsigned)((waves + kRowWaves - 1) / kRowWaves), 2), block(kRowThreads);
+    const int64_t blocks = (waves + kRowWaves - 1) / kRowWaves, wide = 1 << kWide;
+    const dim3 grid((unsigned)(blocks < wide ? blocks : wide), 2, (unsigned)((blocks + wide - 1) / wide)), block(kRowThreads);
     const int n = (int)range;
     if (a.c.int8)
         a.fp16 ? quantized_write_kernel<Fp16, true><<<grid, block, 0, stream>>>(a, n)
