@@ -344,6 +344,35 @@ def test_rows_that_share_memory(n, ld):
     x.check(*x.run(q=dev[0], k=dev[1], v=dev[2]))
 
 
+def test_more_threads_than_one_axis_holds():
+    """16384 sequences of 130 heads, most without a token: their states are zeros, the others' those of a call alone."""
+    seqs, H, at, lens = 16384, 130, [0, 9001, 16383], [70, 1, 130]
+    x = Delta(lens, H, 65, 64, 64, seed=77, initial=False)
+    want, states = x.run()
+    cu = torch.zeros(seqs + 1, dtype=torch.int32)
+    for s, n in zip(at, lens):
+        cu[s + 1:] += n
+    big = torch.full((seqs, H, 64, 64), 7.0, device="cuda")
+    out, big = w.delta_rule(x.q.cuda(), x.k.cuda(), x.v.cuda(), x.g.cuda(), x.beta.cuda(), cu_seqlens=cu.cuda(),
+                            state_out=big)
+    assert torch.equal(out, want) and torch.equal(big[at], states)
+    big[at] = 0
+    assert not any(bool(part.any()) for part in big.split(1024))
+
+
+def test_states_that_are_not_finite():
+    """An infinity or NaN in a first state stays in its column and head."""
+    x = Delta([70, 3], 2, 1, 64, 64, seed=78)
+    out, state = x.run()
+    for bad in (math.nan, math.inf, -math.inf):
+        first = x.state.clone()
+        first[0, 1, 5, 9] = bad
+        o, s = x.run(state=first.cuda())
+        assert not bool(torch.isfinite(o[:70, 1, 9]).any()) and not bool(torch.isfinite(s[0, 1, 5, 9]))
+        o[:70, 1, 9], s[0, 1, :, 9] = out[:70, 1, 9], state[0, 1, :, 9]
+        assert torch.equal(o, out) and torch.equal(s, state)
+
+
 def test_two_streams_at_once():
     """Calls side by side with workspaces of their own."""
     xs = [Delta([300, 70], 4, 2, 128, 64, seed=s) for s in (1, 2)]

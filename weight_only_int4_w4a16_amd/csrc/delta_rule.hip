@@ -150,14 +150,14 @@ void step_typed(const DeltaArgs &a, hipStream_t stream)
 // Decays are summed in float64, and differences of sums taken there.
 //
 // What bounds it: 20000 tokens of 32 heads of 128 (16 for q and k) take 109 us for T and P (0.41 GB: 3.8 TB/s, where a
-// copy of 4 GiB reaches 4.7) and 590 us for the chunks (medians of a trace; 656 us for both by events), a chain of 313
+// copy of 4 GiB reaches 4.7) and 590 us for the chunks (medians of a trace; 658 us for both by events), a chain of 313
 // steps. A copy with the cycle counter read between phases showed 4060 cycles a step in the carrying waves: 1040 on X,
 // 540 on R, 1290 on U, 615 on S and 570 at the three barriers between. By count, their 36 products would take 580 and
 // the 182 KB that a step moves through LDS 1450 at 128 bytes a cycle; the rest is latency. 8 heads, which leave most
-// CUs idle, take 474 us, little less than 32. Steps that counted, whole calls of this size: outputs by waves of their
-// own together with K's other view through LDS and pieces of 8 bytes for V and the outputs 982 -> 720 us; loads before
-// barriers rather than in a phase's middle 781 -> 692 on the way there; S read for the outputs after R and K turned
-// early 661 -> 656; 16 spilled registers in float16 1513 -> 781.
+// CUs idle, take 474 us where 32 take 677 by the same loop. Steps that counted, whole calls of this size: outputs by
+// waves of their own together with K's other view through LDS and pieces of 8 bytes for V and the outputs 982 -> 720
+// us; loads before barriers rather than in a phase's middle 781 -> 692 on the way there; S read for the outputs after R
+// and K turned early 661 -> 656; 16 spilled registers in float16 1513 -> 781.
 constexpr int kDeltaThreads = 256, kWaves = 4;
 constexpr int kFrags = 6;   // operands of a lower triangle: rows 16 w.., columns 32 c.. (c <= w / 2)
 __device__ __forceinline__ constexpr int frag(int w, int c) { return w < 2 ? w : 2 * w - 2 + c; }
@@ -242,18 +242,27 @@ __device__ __forceinline__ float masked(float x, bool keep)
     return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & (keep ? ~0u : 0u));
 }
 
+// Blocks along x, an axis on which a launch holds fewer than 2^32 threads; more of them go along y (2 us of 656 for 20000
+// tokens of 32 heads; with the width read from the grid 11).
+constexpr int kWide = 20;
+
 // Work-groups go to the 8 XCDs in turn, and each XCD has its own L2. Of `groups` that read the same rows, each of
 // `size` work-groups, all of one go to one XCD: group and number inside it of a work-group.
 struct Xcd {
     uint32_t groups, size;
-    __device__ __forceinline__ bool place(uint32_t block, uint32_t *group, uint32_t *inside) const
+    __device__ __forceinline__ bool place(uint32_t *group, uint32_t *inside) const
     {
+        const uint32_t block = blockIdx.y << kWide | blockIdx.x;
         const uint32_t rest = block / 8, eight = rest / size;
         *inside = rest - eight * size;
         *group = eight * 8 + block % 8;
         return *group < groups;
     }
-    int64_t blocks() const { return ((int64_t)groups + 7) / 8 * 8 * size; }
+    dim3 grid() const
+    {
+        const int64_t blocks = ((int64_t)groups + 7) / 8 * 8 * size, wide = 1 << kWide;
+        return blocks <= wide ? dim3((unsigned)blocks) : dim3((unsigned)wide, (unsigned)((blocks + wide - 1) / wide));
+    }
 };
 
 // T and P of one chunk and head. Wave w has rows 16 w ..; products of K rows are formed both ways round, so that
@@ -274,7 +283,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs 
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4;
     uint32_t group, inside;   // a place and head of K, heads that share it
-    if (!xcd.place(blockIdx.x, &group, &inside))
+    if (!xcd.place(&group, &inside))
         return;
     const int32_t place = (int32_t)(group / (uint32_t)a.Hk);
     const int hk = (int)(group - (uint32_t)place * (uint32_t)a.Hk), h = hk * (int)xcd.size + (int)inside;
@@ -906,7 +915,7 @@ __global__ __launch_bounds__(kChunkThreads, 4) void delta_chunk_kernel(DeltaArgs
     __shared__ __align__(16) DeltaLds<Words> lds;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     uint32_t group, inside;   // `heads` heads of a sequence, their slices
-    if (!xcd.place(blockIdx.x, &group, &inside))
+    if (!xcd.place(&group, &inside))
         return;
     const uint32_t slices = xcd.size / (uint32_t)heads, unit = group * (uint32_t)heads + inside / slices;
     const int seq = (int)(unit / (uint32_t)a.H);
@@ -939,13 +948,13 @@ hipError_t delta_of(const DeltaArgs &a, hipStream_t stream)
     const uint32_t share = (uint32_t)(a.H / a.Hk), slices = (uint32_t)a.Dv / 16;
     if (a.T > 0) {
         const Xcd xcd{(uint32_t)(places(a.T, a.B) * a.Hk), share};
-        delta_prepare_kernel<Type, DK><<<dim3((unsigned)xcd.blocks()), dim3(kDeltaThreads), 0, stream>>>(a, work, xcd);
+        delta_prepare_kernel<Type, DK><<<xcd.grid(), dim3(kDeltaThreads), 0, stream>>>(a, work, xcd);
     }
     // Heads that share K and Q together, unless that leaves some of the 8 XCDs with more than 5/4 of the average.
     const uint32_t groups = (uint32_t)a.B * (uint32_t)a.Hk, eights = (groups + 7) / 8;
     const int heads = eights * 32 <= groups * 5 ? (int)share : 1;
     const Xcd xcd{(uint32_t)a.B * (uint32_t)a.H / (uint32_t)heads, slices * (uint32_t)heads};
-    delta_chunk_kernel<Type, DK><<<dim3((unsigned)xcd.blocks()), dim3(kChunkThreads), 0, stream>>>(a, work, xcd, heads);
+    delta_chunk_kernel<Type, DK><<<xcd.grid(), dim3(kChunkThreads), 0, stream>>>(a, work, xcd, heads);
     return hipGetLastError();
 }
 
