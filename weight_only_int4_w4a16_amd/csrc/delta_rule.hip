@@ -14,7 +14,7 @@ namespace {
 // one sum over the row groups; with d = e^g they give u = beta (v - d S^T k) and o = d S^T q + (q . k) u.
 //
 // As for linear attention's single token, 32 columns to a work-group below 128 of (request, head), a whole state
-// and streaming loads and stores from there on: 1 request of 32 heads 3.9 us, 250 requests 174 to 185 us (5.7 to 6.1
+// and streaming loads and stores from there on: 1 request of 32 heads 3.8 us, 250 requests 173 to 186 us (5.7 to 6.1
 // TB/s).
 constexpr int kStepThreads = 256;
 
@@ -150,7 +150,7 @@ void step_typed(const DeltaArgs &a, hipStream_t stream)
 // Decays are summed in float64, and differences of sums taken there.
 //
 // What bounds it: 20000 tokens of 32 heads of 128 (16 for q and k) take 109 us for T and P (0.41 GB: 3.8 TB/s, where a
-// copy of 4 GiB reaches 4.7) and 590 us for the chunks (medians of a trace; 658 us for both by events), a chain of 313
+// copy of 4 GiB reaches 4.7) and 594 us for the chunks (medians of a trace; 658 us for both by events), a chain of 313
 // steps. A copy with the cycle counter read between phases showed 4060 cycles a step in the carrying waves: 1040 on X,
 // 540 on R, 1290 on U, 615 on S and 570 at the three barriers between. By count, their 36 products would take 580 and
 // the 182 KB that a step moves through LDS 1450 at 128 bytes a cycle; the rest is latency. 8 heads, which leave most

@@ -4,7 +4,7 @@
 //   held becomes code * s / s'.     read: code * s, rounded once.
 // Both are bound by memory: 2 bytes read and 1 written per value, or 1 and 2.
 // Measured with 8 heads of 128: 12257 tokens of 40 requests written as e4m3 27 us (2.8 TB/s: a wave's slots, rows,
-// maximum and stores come one after the other, and counters show the vector units busy for 48 % of it), 15 tokens 4.7 us;
+// maximum and stores come one after the other, and counters show the vector units busy for 48 % of it), 15 tokens 4.6 us;
 // 60000 tokens read 84 us (4.4 TB/s, where a copy of 4 GiB reaches 4.7), 500 of 4 heads 3 us.
 //
 // Roundings go by the exact quotients and products. Scales come from the values, so quotients on a border
