@@ -425,8 +425,8 @@ w4a16_status_t w4a16_linear_attention_step(const void *q, int64_t ldq, int64_t h
  *   limits; num_seqs * H <= 2^26; and cu_seqlens has to be non-decreasing (entries are clamped to [0, T]; tokens and
  *   states of a list that decreases get undefined values).
  *   States, decays and sums are held in float32 or more, and the operands of all products that reach a state
- *   as sums of three bfloat16 values (24 bits). What reaches the outputs only is rounded to one bfloat16 (the
- *   scores) or two (16 bits; float16 inputs: two everywhere). A k, v, beta or decay that is not finite (a decay
+ *   as sums of three bfloat16 values (24 bits). What reaches the outputs only is rounded to a sum of two
+ *   (16 bits). A k, v, beta or decay that is not finite (a decay
  *   of -inf is fine) makes NaN of what it reaches: for v its column, else all columns, from its token on. Repeated
  *   calls give identical bits.
  */

@@ -398,7 +398,7 @@ int64_t w4a16_delta_rule_workspace(int32_t T, int32_t num_seqs, int32_t H, int32
     if (T < 0 || T > 0x7FFFFFFF - 64 || num_seqs < 1 || num_seqs > kMaxRequests || !known_linear(1, H, Dk, Dv) ||
         (int64_t)num_seqs * H > kMaxHeads || (type != W4A16_BF16 && type != W4A16_FP16))
         return -1;
-    return delta_workspace(T, num_seqs, H, type);
+    return delta_workspace(T, num_seqs, H);
 }
 
 w4a16_status_t w4a16_delta_rule(const void *q, int64_t ldq, int64_t hsq, const void *k, int64_t ldk, int64_t hsk,

@@ -145,8 +145,9 @@ void step_typed(const DeltaArgs &a, hipStream_t stream)
 // as sums of three bfloat16 values, of which the products above 2^-24 of the whole are taken: 3 where K, which is
 // bfloat16, is the other operand, 6 for T R. float32 products would take 16 times a bfloat16 one's time. Float16 K and Q
 // are sums of two (5 products); with float16 operands the state's columns would need factors of their own, found
-// from chunk to chunk. The outputs take two values of S and U, and P as one (float16: two). Errors against float64 over
-// 20000 tokens: states 1.0e-7 of the norm (in float32 throughout 1.4e-7), outputs 2.2e-3 (their own rounding 1.66e-3).
+// from chunk to chunk. The outputs take two values of S, U and P. Errors against float64 over 20000 tokens: states
+// 1.0e-7 of the norm (in float32 throughout 1.4e-7); outputs are off by their own rounding alone, 1.66e-3 (with one value of
+// P 2.2e-3, at 20000 tokens of 32 heads in 657 us instead of 692: 11 of these are 6 KB more to write per chunk and head).
 // Decays are summed in float64, and differences of sums taken there.
 //
 // What bounds it: 20000 tokens of 32 heads of 128 (16 for q and k) take 109 us for T and P (0.41 GB: 3.8 TB/s, where a
@@ -172,16 +173,15 @@ __device__ __forceinline__ u32x2 take4(f32x4 &v)
 }
 
 // What a chunk of a head needs besides its rows, in the workspace.
-template <class Type>
+constexpr int kScoreTerms = 2;
 struct Prepared {
-    static constexpr int p_terms = __is_same(Type, Fp16) ? 2 : 1;
-    u32x4 t[3][kFrags][64], p[p_terms][kFrags][64];   // first operands: T in three bfloat16 terms, P
+    u32x4 t[3][kFrags][64], p[kScoreTerms][kFrags][64];   // first operands: T in three bfloat16 terms, P in two
     float eb[kChunk], ed[kChunk];                     // e^b, e^(b_63 - b)
     int32_t bad;                                      // first token with a k, beta or decay that is not finite, or 64
     float whole;                                      // e^b_63
     int32_t pad[30];
 };
-static_assert(sizeof(Prepared<Bf16>) % 128 == 0 && sizeof(Prepared<Fp16>) % 128 == 0, "whole cache lines");
+static_assert(sizeof(Prepared) % 128 == 0, "whole cache lines");
 
 // Sequence s has its chunks' places from here on: as many as it has chunks, or more, lie before the next one's.
 __device__ __forceinline__ int32_t first_place(const DeltaArgs &a, int s)
@@ -272,7 +272,7 @@ struct Xcd {
 // (K of the other waves through LDS, sums of decays by vectors: 140 -> 117 us for 10016 of them; heads that share K on
 // one XCD: 107.) Alone, for one chunk, it takes 7.5 us: a chain of loads, 15 steps of substitution and 9 products in turn.
 template <class Type, int DK>
-__global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs a, Prepared<Type> *work, Xcd xcd)
+__global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs a, Prepared *work, Xcd xcd)
 {
     constexpr int C = DK / 32;
     __shared__ u32x4 lds_k[kWaves - 1][C][64];
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs 
     if (!chunk_at(a, place, &t0, &t1))
         return;
     const int32_t n = min(t1 - t0, kChunk);
-    Prepared<Type> &to = work[(int64_t)place * a.H + h];
+    Prepared &to = work[(int64_t)place * a.H + h];
 
     const int32_t ldq = (int32_t)a.ldq, ldk = (int32_t)a.ldk;   // below 2^24
     const Rows kr = rows_of((const uint16_t *)a.k + hk * a.hsk + (int64_t)t0 * ldk, n, ldk, DK, 2);
@@ -352,7 +352,7 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs 
     const f64x4 bi = *(const f64x4 *)&lds_b[16 * w + 4 * g];
     const f32x4 beta_i = *(const f32x4 *)&lds_beta[16 * w + 4 * g];
     f32x4 own = {0.0f, 0.0f, 0.0f, 0.0f};
-    u32x4 p[Prepared<Type>::p_terms][2] = {};
+    u32x4 p[kScoreTerms][2] = {};
 #pragma unroll
     for (int j = 0; j < kWaves; ++j) {
         if (j > w)
@@ -379,14 +379,14 @@ __global__ __launch_bounds__(kDeltaThreads) void delta_prepare_kernel(DeltaArgs 
         }
         lds_a[w * (w + 1) / 2 + j][lane] = x;
 #pragma unroll
-        for (int term = 0; term < Prepared<Type>::p_terms; ++term) {
+        for (int term = 0; term < kScoreTerms; ++term) {
             const u32x2 o = take4(y);
             p[term][j / 2][2 * (j & 1)] = o[0];
             p[term][j / 2][2 * (j & 1) + 1] = o[1];
         }
     }
 #pragma unroll
-    for (int term = 0; term < Prepared<Type>::p_terms; ++term)
+    for (int term = 0; term < kScoreTerms; ++term)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
             if (c <= w / 2)
@@ -527,9 +527,9 @@ struct DeltaUnit {
 // multiplies K by them as they are: a lane's values of S are the second operand's, for the same dims of a K row. The
 // four sums of X meet in LDS; wave w takes the tokens 16 w .. on to R and U, which all need.
 template <class Type, int DK, class Lds>
-__device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<Type> *from, const DeltaUnit &d, int w, Lds &lds)
+__device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared *from, const DeltaUnit &d, int w, Lds &lds)
 {
-    constexpr int EK = DK / 64, NW = 2 * EK, KT = Split<Type>::terms, PT = Prepared<Type>::p_terms;
+    constexpr int EK = DK / 64, NW = 2 * EK, KT = Split<Type>::terms;
     constexpr int SIDE = KT == 1 ? kWaves : 2;   // tiles of X side by side, as many as registers allow
     typedef typename WordsOf<NW>::T Words;
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
@@ -563,7 +563,7 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
     };
     auto prepared = [&](int32_t t) {   // zeros past the last chunk; operands that are none lie past its end
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>((const void *)from), 0,
-                                                 t < t1 ? sizeof(Prepared<Type>) : 0, 0x00027000);
+                                                 t < t1 ? sizeof(Prepared) : 0, 0x00027000);
     };
     auto fetch_t = [&](Rows x) {
 #pragma unroll
@@ -573,7 +573,7 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
                 tn[i][c] = load4(x, c <= w / 2 ? (uint32_t)((i * kFrags + frag(w, c)) * 64 + lane) * 16 : ~0u);
     };
     auto fetch_factors = [&](Rows x) {
-        constexpr uint32_t at = (3 + PT) * kFrags * 64 * 16;
+        constexpr uint32_t at = (3 + kScoreTerms) * kFrags * 64 * 16;
         ebn = __builtin_bit_cast(f32x4, load4(x, at + 4 * (16 * w + 4 * g)));
         edn = __builtin_bit_cast(f32x4, load4(x, at + 4 * (kChunk + 16 * w + 4 * g)));
         endn = __builtin_amdgcn_raw_buffer_load_b64(x, at + 8 * kChunk, 0, 0);
@@ -774,9 +774,9 @@ __device__ __forceinline__ void carry_state(const DeltaArgs &a, const Prepared<T
 // Waves 4 to 7 make the outputs, next to the others on their SIMDs: wave 4 + w those of the tokens 16 w .., transposed,
 // so that a lane has four columns of one token. They also bring V to the others, as float32.
 template <class Type, int DK, class Lds>
-__device__ __forceinline__ void make_outputs(const DeltaArgs &a, const Prepared<Type> *from, const DeltaUnit &d, int w, Lds &lds)
+__device__ __forceinline__ void make_outputs(const DeltaArgs &a, const Prepared *from, const DeltaUnit &d, int w, Lds &lds)
 {
-    constexpr int EK = DK / 64, NW = 2 * EK, KT = Split<Type>::terms, PT = Prepared<Type>::p_terms;
+    constexpr int EK = DK / 64, NW = 2 * EK, KT = Split<Type>::terms;
     typedef typename WordsOf<NW>::T Words;
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4, token = 16 * w + col;
     const int32_t t0 = d.t0, t1 = d.t1;
@@ -784,14 +784,14 @@ __device__ __forceinline__ void make_outputs(const DeltaArgs &a, const Prepared<
     uint16_t *op = (uint16_t *)a.out + d.h * a.hso + d.c0;
     const int32_t ldq = (int32_t)a.ldq, ldv = (int32_t)a.ldv, ldo = (int32_t)a.ldo;
     Words qn[kWaves];   // dims of wave i from 4 EK g on
-    u32x4 pn[PT][2];
+    u32x4 pn[kScoreTerms][2];
     u32x2 vn;           // columns 4 g ..
     float ebn = 0.0f;
     int32_t badn = kChunk;
-    constexpr uint32_t at = (3 + PT) * kFrags * 64 * 16;
+    constexpr uint32_t at = (3 + kScoreTerms) * kFrags * 64 * 16;
     auto prepared = [&](int32_t t) {
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>((const void *)from), 0,
-                                                 t < t1 ? sizeof(Prepared<Type>) : 0, 0x00027000);
+                                                 t < t1 ? sizeof(Prepared) : 0, 0x00027000);
     };
     auto fetch_v = [&](int32_t t) {
         vn = WordsOf<2>::load(rows_of(vp + (int64_t)t * ldv, t1 - t, ldv, 16, 2), 2 * (token * (uint32_t)ldv + 4 * g));
@@ -806,7 +806,7 @@ __device__ __forceinline__ void make_outputs(const DeltaArgs &a, const Prepared<
     };
     auto fetch_p = [&](Rows x) {
 #pragma unroll
-        for (int i = 0; i < PT; ++i)
+        for (int i = 0; i < kScoreTerms; ++i)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
                 pn[i][c] = load4(x, c <= w / 2 ? (uint32_t)(((3 + i) * kFrags + frag(w, c)) * 64 + lane) * 16 : ~0u);
@@ -885,8 +885,8 @@ __device__ __forceinline__ void make_outputs(const DeltaArgs &a, const Prepared<
 #pragma unroll
                 for (int term = 0; term < 2; ++term)
                     ub[c][term] = *(const u32x4 *)lds.uo[term][c][lane];
-            products<2, PT, 1, 2>([&](int c, int term) { return ub[c][term]; },
-                                  [&](int c, int term) { return pn[term][c]; }, o);
+            products<2, kScoreTerms, 1, 2>([&](int c, int term) { return ub[c][term]; },
+                                           [&](int c, int term) { return pn[term][c]; }, o);
         }
         fetch_p(next);
 #pragma unroll
@@ -908,7 +908,7 @@ __device__ __forceinline__ void make_outputs(const DeltaArgs &a, const Prepared<
 constexpr int kChunkThreads = 512;
 
 template <class Type, int DK>
-__global__ __launch_bounds__(kChunkThreads, 4) void delta_chunk_kernel(DeltaArgs a, const Prepared<Type> *work, Xcd xcd,
+__global__ __launch_bounds__(kChunkThreads, 4) void delta_chunk_kernel(DeltaArgs a, const Prepared *work, Xcd xcd,
                                                                        int heads)
 {
     typedef typename WordsOf<DK / 32>::T Words;
@@ -925,7 +925,7 @@ __global__ __launch_bounds__(kChunkThreads, 4) void delta_chunk_kernel(DeltaArgs
     d.hk = d.h / (a.H / a.Hk);
     d.c0 = (int)(inside % slices) * 16;
     tokens_of(a, seq, &d.t0, &d.t1);
-    const Prepared<Type> *from = work + (int64_t)__builtin_amdgcn_readfirstlane(first_place(a, seq)) * a.H + d.h;
+    const Prepared *from = work + (int64_t)__builtin_amdgcn_readfirstlane(first_place(a, seq)) * a.H + d.h;
     if (tid < 32)
         lds.bad[tid >> 4][tid & 15] = kChunk;
     if (tid < 2)
@@ -944,7 +944,7 @@ int64_t places(int32_t T, int32_t num_seqs) { return num_seqs == 1 ? ((int64_t)T
 template <class Type, int DK>
 hipError_t delta_of(const DeltaArgs &a, hipStream_t stream)
 {
-    Prepared<Type> *work = (Prepared<Type> *)a.work;
+    Prepared *work = (Prepared *)a.work;
     const uint32_t share = (uint32_t)(a.H / a.Hk), slices = (uint32_t)a.Dv / 16;
     if (a.T > 0) {
         const Xcd xcd{(uint32_t)(places(a.T, a.B) * a.Hk), share};
@@ -960,11 +960,11 @@ hipError_t delta_of(const DeltaArgs &a, hipStream_t stream)
 
 }  // namespace
 
-int64_t delta_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t type)
+int64_t delta_workspace(int32_t T, int32_t num_seqs, int32_t H)
 {
-    if (places(T, num_seqs) * H > 1 << 30)   // 25 TB of them
+    if (places(T, num_seqs) * H > 1 << 30)   // 34 TB of them
         return -1;
-    return places(T, num_seqs) * H * (int64_t)(type ? sizeof(Prepared<Fp16>) : sizeof(Prepared<Bf16>));
+    return places(T, num_seqs) * H * (int64_t)sizeof(Prepared);
 }
 
 hipError_t launch_delta(const DeltaArgs &a, hipStream_t stream)

@@ -100,6 +100,6 @@ int64_t attention_workspace(int32_t Hq, int32_t heads, int32_t dim);
 // Most units of work of one request and head.
 int64_t attention_units(int32_t max_pages, int32_t page_size);
 int64_t linear_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk, int32_t Dv);
-int64_t delta_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t type);
+int64_t delta_workspace(int32_t T, int32_t num_seqs, int32_t H);
 
 }  // namespace w4a16
