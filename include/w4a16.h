@@ -506,7 +506,7 @@ w4a16_status_t w4a16_quantized_kv_read(const w4a16_quantized_cache_t *cache, con
 /*
  * w4a16_paged_attention over such a cache: the same operands, masks, limits and results. Products and sums are
  * held in float32; the probabilities, times the scale of their value, enter their product with the codes as
- * float16 (11 bits down to 2^-29 of the largest, and nothing below 2^-40 of it), for both types of activations;
+ * sums of two float16 (22 bits down to 2^-18 of the largest, and nothing below 2^-40 of it), for both types of activations;
  * bfloat16 queries enter theirs as float16 times a power of two (exact down to 2^-32 of a head's largest
  * magnitude). Scales of blocks without a position that is read may be anything. A scale that is NaN makes NaN of
  * the requests and heads that read a position of its block (of keys: lse as well).

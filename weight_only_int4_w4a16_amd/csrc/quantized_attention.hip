@@ -12,8 +12,10 @@
 // permute, which makes 1024 + 128 + code of it, and one packed subtraction: 5 operations for 4 codes.
 //
 // A value's scale goes with its weight, e^{s_j} vs_b, and float16 has little range: the reference of these
-// weights is the running maximum of s_j + log vs_b, less 15 powers of two (11 bits down to 2^-29 of the largest
-// one). The weights' own sum has another reference, the maximum of s_j, and is held in float32 without rounding.
+// weights is the running maximum of s_j + log vs_b, less 15 powers of two. They enter as two float16 values (22 bits
+// down to 2^-18 of the largest one): with one, float16 outputs were off by 2.74e-4 of their norm where their own
+// rounding is 2.06e-4 (48 requests of up to 5000), for 85.4 us instead of 88.5 (64 ragged requests of up to 8192). The
+// weights' own sum has another reference, the maximum of s_j, and is held in float32 without rounding.
 //
 // The cache's bytes bound it. 64 ragged requests of up to 8192 positions, 64 heads on 8 of 128, int8: 82 us and 5 joining
 // (medians of a trace; 83 in all by events; 0.44 GB: 5.3 TB/s here, where a streaming read of 4 GiB reaches 6.3); one
@@ -294,10 +296,15 @@ __global__ __launch_bounds__(kThreads, 2) void quantized_attention_kernel(Quanti
                 total += __builtin_amdgcn_exp2f(x[e] - ref);
                 y[e] = __builtin_amdgcn_exp2f(y[e] - o_ref);
             }
-            u32x4 p;   // the weights with the values' scales, at most 2^15, as float16
+            u32x4 p, rest;   // the weights with the values' scales, at most 2^15, as float16, and what that leaves
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                p[e] = pack2(Fp16(), y[2 * e], y[2 * e + 1]);
+            for (int e = 0; e < 4; ++e) {
+                uint32_t both = pack2(Fp16(), y[2 * e], y[2 * e + 1]);
+                asm volatile("" : "+v"(both));   // or the remainder converts once more
+                const f16x2 x = __builtin_bit_cast(f16x2, both);
+                p[e] = both;
+                rest[e] = pack2(Fp16(), y[2 * e] - (float)x[0], y[2 * e + 1] - (float)x[1]);
+            }
             if (__ballot(fade != 1.0f)) {
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
@@ -321,6 +328,9 @@ __global__ __launch_bounds__(kThreads, 2) void quantized_attention_kernel(Quanti
 #pragma unroll
                 for (int j = 4 * w; j < 4 * w + 4 && j < D / 16; ++j)
                     o[j] = mfma(Fp16(), v[j & 3], p, o[j]);
+#pragma unroll
+                for (int j = 4 * w; j < 4 * w + 4 && j < D / 16; ++j)
+                    o[j] = mfma(Fp16(), v[j & 3], rest, o[j]);
             }
         }
 
