@@ -29,3 +29,19 @@ def test_outputs_are_off_by_their_own_rounding(kind, dtype):
     got = float((out.cpu().double() - want).norm() / want.norm())
     print(f"{own:.4g} {got:.4g}")
     assert got <= own + 2.0 ** -16
+
+
+@pytest.mark.parametrize("kind", [I8, E4])
+@pytest.mark.parametrize("down", [100, 108, 114])
+def test_values_near_the_least_scale(kind, down):
+    """Values' scales down to 2^-126: results are those of the same codes with larger scales, times a power of two, but
+    for half a step of bfloat16 below its normal numbers (2^-134)."""
+    x = Attend([300, 40, 1, 700], 8, 2, 64, 32, 16, kind, BF, seed=31)
+    larger = x.scale[1]
+    x.scale[1] = (larger * 2.0 ** -down).clamp(min=2.0 ** -126)
+    out, lse = x.run()
+    x.scale[1] = x.scale[1] * 2.0 ** down
+    assert float((x.scale[1] - larger).abs().max()) < 2.0 ** (down - 120)
+    assert bool(out.any(-1).all())
+    got = out.cpu().double() * 2.0 ** down
+    x.check(got, lse)

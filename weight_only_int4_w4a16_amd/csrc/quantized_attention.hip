@@ -336,7 +336,8 @@ __global__ __launch_bounds__(kThreads, 2) void quantized_attention_kernel(Quanti
 
         // Join the four waves in LDS. A lane holds, of head col, dims of V lane 4g + k (k < 4).
         total = sum4(total);
-        const float even = o_top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(o_top - top);   // one reference again
+        // One reference again, in two halves: exp2 gives zero below 2^-126, and value scales go down to that themselves.
+        const float half_even = o_top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(0.5f * (o_top - top));
         __syncthreads();   // the scan's sums, or the previous piece's, have been read
         if (g == 0) {
             tops[wave][col] = top;
@@ -346,7 +347,8 @@ __global__ __launch_bounds__(kThreads, 2) void quantized_attention_kernel(Quanti
         for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int j = 0; j < D / 16; j += 2)
-                *(f32x2 *)&sums[wave][col][P::dim(4 * g + k, j)] = f32x2{o[j][k] * even, o[j + 1][k] * even};
+                *(f32x2 *)&sums[wave][col][P::dim(4 * g + k, j)] =
+                    f32x2{o[j][k] * half_even * half_even, o[j + 1][k] * half_even * half_even};
         __syncthreads();
         const bool whole = t0 == 0 && count == span.units;
         const int piece = 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0);
