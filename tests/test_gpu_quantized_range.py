@@ -1,4 +1,6 @@
 """Attention over the 8-bit cache: digits of its results, and values and scales of every size."""
+import math
+
 import pytest
 import torch
 
@@ -45,3 +47,24 @@ def test_values_near_the_least_scale(kind, down):
     assert bool(out.any(-1).all())
     got = out.cpu().double() * 2.0 ** down
     x.check(got, lse)
+
+
+@pytest.mark.parametrize("kind", [I8, E4])
+@pytest.mark.parametrize("dtype,base", [(FP, -10), (BF, -10), (BF, -45), (BF, 17)])
+def test_weights_and_scales_far_apart(kind, dtype, base):
+    """One block has the larger weights by 2^30, the other the larger values by 2^30, so that both count alike. Weights alone
+    leave float16's range, and so do their products with the scales, which are 2^-45 or 2^17 here."""
+    x = Attend([32], 1, 1, 64, 16, 16, kind, dtype, seed=32)
+    x.q[:] = 1.0
+    p = x.table[0, :2].long()
+    x.codes[0] = torch.zeros_like(x.codes[0])
+    x.codes[0][p[0], :, :, 0] = torch.tensor(96.0).to(kind)          # a value of both
+    x.scale[0][:] = 1.0
+    x.scale[1][p[0]], x.scale[1][p[1]] = 2.0 ** base, 2.0 ** (base + 30)
+    scale = 30 * math.log(2) / 96
+    out, lse = x.run(scale=scale)
+    x.check(out, lse, scale=scale)
+    x.codes[1][p[0]] = torch.zeros_like(x.codes[1][p[0]])             # the second block alone
+    one, _ = x.run(scale=scale)
+    assert bool((one != out).any()) and bool(one.any())
+    x.check(one, lse, scale=scale)
