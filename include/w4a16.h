@@ -445,7 +445,7 @@ int64_t w4a16_delta_rule_workspace(int32_t T, int32_t num_seqs, int32_t H, int32
 /*
  * The recurrent form of w4a16_delta_rule for one new token of each of B requests, as
  * w4a16_linear_attention_step is of w4a16_linear_attention: states by slots, in place or not. All
- * arithmetic is float32.
+ * arithmetic is float32; what is not finite makes NaN of the same columns, of the request's state and output.
  */
 w4a16_status_t w4a16_delta_rule_step(const void *q, int64_t ldq, int64_t hsq, const void *k, int64_t ldk,
                                      int64_t hsk, const void *v, int64_t ldv, int64_t hsv, const float *log_decay,

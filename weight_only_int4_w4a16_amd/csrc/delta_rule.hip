@@ -16,7 +16,12 @@ namespace {
 // As for linear attention's single token, 32 columns to a work-group below 128 of (request, head), a whole state
 // and streaming loads and stores from there on: 1 request of 32 heads 3.8 us, 250 requests 173 to 186 us (5.7 to 6.1
 // TB/s).
+//
+// What is not finite counts as NaN, so that it reaches the same places as in packed sequences: an infinite k_i, v, beta or
+// decay would leave zeros and infinities in the state.
 constexpr int kStepThreads = 256;
+
+__device__ __forceinline__ float finite_or_nan(float x) { return fabsf(x) < INFINITY ? x : NAN; }
 
 template <class Type, int DK, int DV, int CV, bool STREAM>
 __global__ __launch_bounds__(kStepThreads) void delta_step_kernel(DeltaArgs a)
@@ -46,14 +51,15 @@ __global__ __launch_bounds__(kStepThreads) void delta_step_kernel(DeltaArgs a)
     const int hk = h / (a.H / a.Hk);
     if (tid < DK) {
         qs[tid] = Type::f(((const T *)a.q)[b * a.ldq + hk * a.hsq + tid]);
-        ks[tid] = Type::f(((const T *)a.k)[b * a.ldk + hk * a.hsk + tid]);
+        ks[tid] = finite_or_nan(Type::f(((const T *)a.k)[b * a.ldk + hk * a.hsk + tid]));
     }
     const T *vp = (const T *)a.v + b * a.ldv + h * a.hsv + c0;
     f32x4 v, sk = {0.0f, 0.0f, 0.0f, 0.0f}, sq = sk;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        v[e] = Type::f(vp[e]);
-    const float decay = expf(a.g[b * a.ldg + h * a.hsg]), beta = a.beta[b * a.ldb + h * a.hsb];
+        v[e] = finite_or_nan(Type::f(vp[e]));
+    const float g = a.g[b * a.ldg + h * a.hsg], decay = g < INFINITY ? expf(g) : NAN;
+    const float beta = finite_or_nan(a.beta[b * a.ldb + h * a.hsb]);
     __syncthreads();
     float qk = 0.0f;   // every wave sums all of q . k
     for (int i = tid & 63; i < DK; i += 64)
