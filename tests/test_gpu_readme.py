@@ -38,3 +38,21 @@ def test_readme_lines_run():
     assert names["y"].shape == (64,) and names["o"].shape == (3, 2, 64)
     assert names["t"].slot_map.tolist() == [0, 5 * 16 + 15, 16]
     assert bool(names["state"].ne(0).any())
+
+
+def test_readme_delta_line_keeps_states_bounded():
+    """The line that steps the delta rule, again and again over the same tokens as the README's. With keys of norm 1 and beta
+    and decays below 1 a state's column shrinks by e^-0.1 a step and grows by at most 0.91 |v|: its norm stays below 9.6 max |v|."""
+    with open(README) as f:
+        text = f.read()
+    line = re.findall(r"^o = w\.delta_rule_step\(.*$", text, re.M)
+    keys = re.findall(r"^kn = .*$", text, re.M)
+    assert len(line) == 1
+    torch.manual_seed(1)
+    names = dict(torch=torch, w=w, log_decay=torch.full((2,), -0.1, device="cuda"), beta=torch.full((2,), 0.9, device="cuda"),
+                 state=torch.zeros(3, 2, 64, 64, device="cuda"))
+    names.update({n: torch.randn(3, 2, 64, device="cuda").to(torch.bfloat16) for n in "kvq"})
+    for _ in range(200):
+        for x in keys + line:
+            exec(x, names)
+    assert float(names["state"].norm(dim=2).max()) <= 9.6 * float(names["v"].float().abs().max())
