@@ -27,7 +27,7 @@ def _rates(beta, T: int, H: int, dev: int):
 
 def delta_rule_workspace(q: torch.Tensor, v: torch.Tensor, num_seqs: int = 1) -> torch.Tensor:
     """Scratch memory for delta_rule over the tokens of q and v in `num_seqs` sequences, or over fewer tokens or
-    sequences."""
+    sequences: 31 KB for every 64 tokens and head (2 GB for 131072 tokens of 32 heads), and for every sequence and head."""
     need = _library().w4a16_delta_rule_workspace(q.shape[0], num_seqs, v.shape[1], q.shape[2], v.shape[2], _TYPES[q.dtype])
     return torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
 
@@ -41,9 +41,11 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: tor
 
     q, k [T, Hk, Dk] and v [T, H, Dv] bfloat16 or float16 (head h reads q and k of head h / (H / Hk); keys
     of norm 1 are meant); log_decay and beta float32 [T, H], or [H] where fixed for each head; cu_seqlens int32
-    [num_seqs + 1] on the GPU, or None for one sequence; state float32 [num_seqs, H, Dk, Dv], or None for zeros.
+    [num_seqs + 1] on the GPU, or None for one sequence: not decreasing (linear_attention makes its own so, here tokens
+    and states of a list that decreases are undefined), and clamped to the tokens; state float32 [num_seqs, H, Dk, Dv], or None for zeros.
     scale defaults to Dk ** -0.5. Returns (out [T, H, Dv], state_out), where state_out may be `state` itself.
-    `workspace` (delta_rule_workspace) may be kept for all calls on one stream."""
+    `workspace` (delta_rule_workspace, 31 KB for every 64 tokens and head) may be kept for all calls on one stream;
+    without it a call allocates that much."""
     if out is not None and state_out is not None and workspace is not None and stream is None:
         _library()
         if _short(mixers._binding.delta_rule(q, k, v, log_decay, beta, cu_seqlens, state, state_out, _factor(scale, q),
