@@ -463,7 +463,9 @@ w4a16_status_t w4a16_delta_rule_step(const void *q, int64_t ldq, int64_t hsq, co
  *   block 16, 32, 48 or 64 and page_size a multiple of it; dim 64, 96, 128, 192 or 256; num_pages, page_size,
  *   heads as in w4a16_paged_cache_t. k, v 16-byte aligned, their strides multiples of 16, slot strides 0 to
  *   2^24 - 1. Scale strides are free.
- * The scales are written by w4a16_quantized_kv_write; before that, codes and scales may be anything.
+ * The scales are written by w4a16_quantized_kv_write: 2^-126 or more, or NaN. Before that, codes and scales of blocks
+ * that are not read may be anything. Scales that come from elsewhere are zero or more, or NaN: with a negative one
+ * reads give values without its sign, and attention gives NaN.
  */
 typedef struct {
     void *k, *v;
@@ -485,8 +487,9 @@ typedef struct {
  * become code * s / s', rounded in the same way. A run that starts a block drops what the block held: codes of
  * slots behind it are left as they are and stand for nothing.
  *   So a sequence is written from its first position on, in any number of calls, and may be taken back to any
- *   length and continued. Runs of one call lie in different blocks (two of them in one leave it undefined, and
- *   touch nothing else).
+ *   length and continued; one that begins in a block's middle has the scale that the block had before, at least,
+ *   whoever wrote it. Runs of one call lie in different blocks (two of them in one leave it undefined, and touch
+ *   nothing else).
  *   Where a run's row holds a value that is not finite, the scale becomes NaN and the run's codes zero: the whole
  *   block and head then reads as NaN, until it is started anew.
  *   0 <= T, T * heads <= 2^35; k, v of `type` W4A16_BF16 or W4A16_FP16, 16-byte aligned, strides multiples of 8.

@@ -42,8 +42,8 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: tor
     q, k [T, Hk, Dk] and v [T, H, Dv] bfloat16 or float16 (head h reads q and k of head h / (H / Hk); keys
     of norm 1 are meant); log_decay and beta float32 [T, H], or [H] where fixed for each head; cu_seqlens int32
     [num_seqs + 1] on the GPU, or None for one sequence: not decreasing (linear_attention makes its own so, here tokens
-    and states of a list that decreases are undefined), and clamped to the tokens; state float32 [num_seqs, H, Dk, Dv], or None for zeros.
-    scale defaults to Dk ** -0.5. Returns (out [T, H, Dv], state_out), where state_out may be `state` itself.
+    and states of a list that decreases are undefined), and clamped to the tokens; state float32 [num_seqs, H, Dk, Dv],
+    or None for zeros. scale defaults to Dk ** -0.5. Returns (out [T, H, Dv], state_out), where state_out may be `state` itself.
     `workspace` (delta_rule_workspace, 31 KB for every 64 tokens and head) may be kept for all calls on one stream;
     without it a call allocates that much."""
     if out is not None and state_out is not None and workspace is not None and stream is None:

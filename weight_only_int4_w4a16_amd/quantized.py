@@ -3,6 +3,9 @@ written, read back, and attended to. Conventions of `mixers`, and
 
   codes   int8 or float8_e4m3fn [pages, page_size, heads, dim], strides as for the caches there
   scales  float32 [pages, page_size / block, heads], any strides; block 16, 32, 48 or 64; value = code * scale
+
+quantized_kv_write makes the scales: 2^-126 or more, or NaN. One that comes from elsewhere must not be negative: its sign
+would be lost on reading, and attention would give NaN.
 """
 from __future__ import annotations
 
@@ -58,9 +61,9 @@ def quantized_kv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, 
     Tokens with slots one after the other in a block are a run, and runs of one call lie in different blocks. A
     run that starts at a block's first slot starts the block anew, with the scale largest |x| / 127 (int8) or / 448
     (e4m3) of each head; another one raises the block's scale where it has to, and the codes that the block holds
-    go over to it. A sequence is thus written from its first position on, in any number of calls. Tokens whose
-    slot is outside the cache are skipped. A value that is not finite makes NaN of its block and head, until
-    the block is started anew."""
+    go over to it. A sequence is thus written from its first position on, in any number of calls (one that begins in a
+    block's middle has the scale that the block had before, at least). Tokens whose slot is outside the cache are
+    skipped. A value that is not finite makes NaN of its block and head, until the block is started anew."""
     if stream is None:
         _library()
         if _short(mixers._binding.quantized_kv_write(k, v, k_cache, v_cache, k_scale, v_scale, slot_map),
