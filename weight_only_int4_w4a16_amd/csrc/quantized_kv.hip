@@ -255,9 +255,10 @@ __global__ __launch_bounds__(kRowThreads) void quantized_read_kernel(QuantizedRo
 
 hipError_t launch_quantized_write(const QuantizedRowsArgs &a, hipStream_t stream)
 {
-    // As many tokens to a wave as leave 8 waves per SIMD (1024 of them), 16 at most: prompts of 12257 tokens with 4, 8,
-    // 16 and 32 to a wave 40.7, 35.2, 30.2 and 30.3 us (the least of 6, before later steps), while single tokens of
-    // many requests, each a run, want waves of their own.
+    // As many tokens to a wave as leave 8192 waves in the launch, 8 for each SIMD (their registers let 5 of them reside
+    // with int8, 4 with e4m3), 16 at most: prompts of 12257 tokens with 4, 8, 16 and 32 to a wave 40.7, 35.2, 30.2 and 30.3
+    // us (the least of 6, before later steps; why 16 and 32 are alike was not found out), while single tokens of many
+    // requests, each a run, want waves of their own.
     int64_t range = (int64_t)a.T * 2 * a.c.heads / 8192;
     range = range < 1 ? 1 : range > 16 ? 16 : range;
     const int64_t waves = (a.T + range - 1) / range * a.c.heads;   // below 2^32: T heads <= 2^35
