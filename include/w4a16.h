@@ -438,8 +438,8 @@ w4a16_status_t w4a16_delta_rule(const void *q, int64_t ldq, int64_t hsq, const v
                                 float *state_out, void *out, int64_t ldo, int64_t hso, void *workspace,
                                 int64_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of workspace for w4a16_delta_rule (host only), -1 where the arguments are out of range. Never less for
- * more tokens or sequences. */
+/* Bytes of workspace for w4a16_delta_rule (host only): 31360 for every head and chunk of up to 64 tokens, and at most one
+ * chunk more for every sequence; -1 where the arguments are out of range. Never less for more tokens or sequences. */
 int64_t w4a16_delta_rule_workspace(int32_t T, int32_t num_seqs, int32_t H, int32_t Dk, int32_t Dv, int32_t type);
 
 /*

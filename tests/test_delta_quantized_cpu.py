@@ -220,3 +220,11 @@ def test_short_way_declines():
         b.bind_more(1, 2)
     with pytest.raises(ValueError):
         b.bind_more(0, 1, 2, 3, 4)
+
+
+def test_workspace_is_as_large_as_said():
+    f = lib().w4a16_delta_rule_workspace
+    for dtype in (0, 1):
+        assert f(64, 1, 1, 128, 128, dtype) == f(1, 1, 1, 64, 64, dtype) == 31360
+        assert f(131072, 1, 32, 128, 128, dtype) == 2048 * 32 * 31360
+        assert f(1000, 7, 4, 128, 64, dtype) <= (-(-1000 // 64) + 7) * 4 * 31360
