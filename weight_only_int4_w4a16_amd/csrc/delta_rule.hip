@@ -14,7 +14,7 @@ namespace {
 // one sum over the row groups; with d = e^g they give u = beta (v - d S^T k) and o = d S^T q + (q . k) u.
 //
 // As for linear attention's single token, 32 columns to a work-group below 128 of (request, head), a whole state
-// and streaming loads and stores from there on: 1 request of 32 heads 3.8 us, 250 requests 173 to 186 us (5.7 to 6.1
+// and streaming loads and stores from there on: 1 request of 32 heads 4.0 us, 250 requests 173 to 186 us (5.7 to 6.1
 // TB/s).
 //
 // What is not finite counts as NaN, so that it reaches the same places as in packed sequences: an infinite k_i, v, beta or
@@ -153,18 +153,18 @@ void step_typed(const DeltaArgs &a, hipStream_t stream)
 // are sums of two (5 products); with float16 operands the state's columns would need factors of their own, found
 // from chunk to chunk. The outputs take two values of S, U and P. Errors against float64 over 20000 tokens: states
 // 1.0e-7 of the norm (in float32 throughout 1.4e-7); outputs are off by their own rounding alone, 1.66e-3 (with one value of
-// P 2.2e-3, at 20000 tokens of 32 heads in 657 us instead of 692: 11 of these are 6 KB more to write per chunk and head).
+// P 2.2e-3, and 657 us for these instead of 692: 15 for 6 KB more to write per chunk and head, 20 for loading it).
 // Decays are summed in float64, and differences of sums taken there.
 //
-// What bounds it: 20000 tokens of 32 heads of 128 (16 for q and k) take 109 us for T and P (0.41 GB: 3.8 TB/s, where a
-// copy of 4 GiB reaches 4.7) and 594 us for the chunks (medians of a trace; 658 us for both by events), a chain of 313
-// steps. A copy with the cycle counter read between phases showed 4060 cycles a step in the carrying waves: 1040 on X,
-// 540 on R, 1290 on U, 615 on S and 570 at the three barriers between. By count, their 36 products would take 580 and
-// the 182 KB that a step moves through LDS 1450 at 128 bytes a cycle; the rest is latency. 8 heads, which leave most
-// CUs idle, take 474 us where 32 take 677 by the same loop. Steps that counted, whole calls of this size: outputs by
-// waves of their own together with K's other view through LDS and pieces of 8 bytes for V and the outputs 982 -> 720
-// us; loads before barriers rather than in a phase's middle 781 -> 692 on the way there; S read for the outputs after R
-// and K turned early 661 -> 656; 16 spilled registers in float16 1513 -> 781.
+// What bounds it: 20000 tokens of 32 heads of 128 (16 for q and k) take 117 us for T and P (0.48 GB: 4.1 TB/s, where a
+// copy of 4 GiB reaches 4.7) and 606 us for the chunks (medians of a trace; 694 us for both by events), a chain of 313
+// steps. A copy with the cycle counter read between phases, and one value of P, showed 4060 cycles a step in the
+// carrying waves: 1040 on X, 540 on R, 1290 on U, 615 on S and 570 at the three barriers between. By count, their 36
+// products would take 580 and the 182 KB that a step moves through LDS 1450 at 128 bytes a cycle; the rest is latency. 8
+// heads, which leave most CUs idle, take 513 us where 32 take 692 by the same loop. Steps that counted, whole calls of this
+// size, with one value of P: outputs by waves of their own together with K's other view through LDS and pieces of 8 bytes
+// for V and the outputs 982 -> 720 us; loads before barriers rather than in a phase's middle 781 -> 692 on the way there; S
+// read for the outputs after R and K turned early 661 -> 656; 16 spilled registers in float16 (2 are left) 1513 -> 781.
 constexpr int kDeltaThreads = 256, kWaves = 4;
 constexpr int kFrags = 6;   // operands of a lower triangle: rows 16 w.., columns 32 c.. (c <= w / 2)
 __device__ __forceinline__ constexpr int frag(int w, int c) { return w < 2 ? w : 2 * w - 2 + c; }

@@ -14,13 +14,14 @@
 // A value's scale goes with its weight, e^{s_j} vs_b, and float16 has little range: the reference of these
 // weights is the running maximum of s_j + log vs_b, less 15 powers of two. They enter as two float16 values (22 bits
 // down to 2^-18 of the largest one): with one, float16 outputs were off by 2.74e-4 of their norm where their own
-// rounding is 2.06e-4 (48 requests of up to 5000), for 85.4 us instead of 88.5 (64 ragged requests of up to 8192). The
+// rounding is 2.06e-4 (48 requests of up to 5000), for 85.4 us instead of 87.1 (64 ragged requests of up to 8192). The
 // weights' own sum has another reference, the maximum of s_j, and is held in float32 without rounding.
 //
-// The cache's bytes bound it. 64 ragged requests of up to 8192 positions, 64 heads on 8 of 128, int8: 82 us and 5 joining
-// (medians of a trace; 83 in all by events; 0.44 GB: 5.3 TB/s here, where a streaming read of 4 GiB reaches 6.3); one
-// request of 131000 positions 54 and 8 us, of 1100 6.8 and 4; 48 requests of up to 5000, e4m3, 26 and 5. By events,
-// three work-groups per CU 87.9 us instead of 84.9, four 133; V a tile ahead as well as K 86 instead of 85.
+// The cache's bytes bound it. 64 ragged requests of up to 8192 positions, 64 heads on 8 of 128, int8: 83 us and 5 joining
+// (medians of a trace; 87 in all by events; 0.44 GB: 5.3 TB/s here, where a streaming read of 4 GiB reaches 6.3); one
+// request of 131000 positions 55 and 8 us, of 1100 7.0 and 4; 48 requests of up to 5000, e4m3, 26 and 5. By events, with
+// one value of the weights, three work-groups per CU 87.9 us instead of 84.9, four 133; V a tile ahead as well as K 86
+// instead of 85.
 #include "attention_runs.h"
 
 namespace w4a16 {
